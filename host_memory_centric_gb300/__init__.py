@@ -154,6 +154,11 @@ def lib():
         "mt_embed_fwd": (i32, [_v, _v, i64, i32, i32, _v, _v]),
         "mt_embed_bwd": (i32, [_v, _v, _v, i32, i32, _v, _v]),
         "mt_cross_entropy": (i32, [_v, _v, i64, i32, f32, _v, _v]),
+        "mt_linear_cross_entropy_scratch_bytes": (sz, [i64, i32, i32, i32]),
+        "mt_linear_cross_entropy": (i32, [_v, _v, _v, i64, i32, i32, f32, _v, _v, _v, _v, sz, _v]),
+        "mt_distill_topk": (i32, [_v, _v, _v, _v, i64, i32, i32, f32, f32, f32, _v, _v, _v, _v]),
+        "mt_router_balance_scratch_bytes": (sz, [i64, i32, i32]),
+        "mt_router_balance": (i32, [_v, _v, _v, i64, i32, i32, i32, f32, f32, _v, _v, _v, _v, _v, sz, _v]),
         "mt_kernel_error": (i32, [_P(i32), i32]),
         "mt_fault_inject": (i32, [i32, i32]),
         "mt_moe_scratch_bytes": (sz, [i64, i32, i32, i32, i32]),

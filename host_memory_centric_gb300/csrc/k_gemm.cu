@@ -106,6 +106,7 @@ struct Params {
   int64_t d_estride;
   int ngrp;
   int grp_e[MAX_EXPERT_GROUPS], grp_k0[MAX_EXPERT_GROUPS], grp_nk[MAX_EXPERT_GROUPS];
+  SoftmaxPieces sp;   // softmax epilogue (gemm_softmax_pieces)
 };
 
 __device__ __forceinline__ uint32_t su32(const void* p) {
@@ -225,6 +226,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Epilogue of 32 consecutive columns of one output row.
 __device__ __forceinline__ void epi_store(const Epi& e, int row, int col, const uint32_t (&r)[32]) {
   float v[32];
@@ -277,6 +285,83 @@ __device__ __forceinline__ void epi_store(const Epi& e, int row, int col, const 
       if (e.D) e.D[(int64_t)row * e.ldd + col + i] = __float2bfloat16_rn(x);
     }
   }
+}
+
+// Softmax epilogue of one row of a 256-column piece of logits (columns col0 ..
+// col0 + 255 of N, in TMEM from taddr on): m = the row's largest logit of the
+// piece, s = sum exp(z - m) over its columns but the target's (which the join
+// adds from zt, so that 1 - p of a confident row is a sum and no difference),
+// both from the FP32 accumulators, to stat[row][piece]; e = bf16(exp(z - m)),
+// if wanted, to E; the target's logit, if it lies in the piece, to zt.  Two passes over the accumulator, since m has
+// to be known before the first exponential: reading TMEM twice costs less than
+// rescaling, and the epilogue hides behind the next tile's MMAs (at K = 3584 a
+// tile's MMAs take about 18 us, its epilogue about 3).  All lanes take part in
+// the loads; rows >= M store nothing.
+template <bool STORE>
+__device__ __forceinline__ void softmax_piece(const SoftmaxPieces& sp, int row, int M, int N, int col0,
+                                              uint32_t taddr) {
+  const bool live = row < M;
+  const int tgt = live ? sp.target[row] : -1;
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < BN / 32; ++c) {
+    const int col = col0 + c * 32;
+    if (col >= N) break;  // warp-uniform
+    uint32_t r[32];
+    tmem_ld32(taddr + (uint32_t)(c * 32), r);
+    if (__any_sync(0xffffffffu, tgt >= col && tgt < col + 32 && tgt < N)) {  // once per row and pass over V
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (tgt == col + i && tgt < N) sp.zt[row] = __uint_as_float(r[i]);
+    }
+    if (col + 32 <= N) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) m = fmaxf(m, __uint_as_float(r[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (col + i < N) m = fmaxf(m, __uint_as_float(r[i]));
+    }
+  }
+  // every logit -inf (or NaN): the reference 0 leaves exp(z) = 0 (or NaN)
+  const float ref = m == -INFINITY ? 0.f : m;
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < BN / 32; ++c) {
+    const int col = col0 + c * 32;
+    if (col >= N) break;
+    uint32_t r[32];
+    tmem_ld32(taddr + (uint32_t)(c * 32), r);
+    float v[32];
+    // z - m first, exact for the terms that count, then the factor log2(e): a
+    // fused z log2(e) - m log2(e) would lose digits where |z| is large
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = exp2_approx((__uint_as_float(r[i]) - ref) * kLog2e);
+    if (col + 32 > N) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (col + i >= N) v[i] = 0.f;
+    }
+    if (__any_sync(0xffffffffu, tgt >= col && tgt < col + 32)) {  // the target's own column is overwritten by the join
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (tgt == col + i) v[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      s0 += v[i];
+      s1 += v[i + 1];
+    }
+    if (STORE && live) {
+      uint4* p = reinterpret_cast<uint4*>(sp.E + (int64_t)row * sp.ldE + col);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col + 8 * i < N)  // ldE is N rounded up to 8 columns at least: a started vector fits the row
+          p[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                            pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+    }
+  }
+  if (live) sp.stat[(int64_t)row * sp.npieces + col0 / BN] = make_float2(ref, s0 + s1);
 }
 
 // Producer side of one output tile: its K-blocks into the shared-memory ring.
@@ -722,7 +807,9 @@ __device__ __forceinline__ void st_cluster_s32(uint32_t addr, int v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-template <int NG, bool A0, bool B0, bool A1, bool B1, int NW = 1>
+// EPI 0: the plain epilogue (epi_store); 1 and 2: the softmax epilogue of a
+// narrow (256 x 256) tile, without and with the exponentials stored.
+template <int NG, bool A0, bool B0, bool A1, bool B1, int NW = 1, int EPI = 0>
 __global__ void __launch_bounds__(THREADS, 1) gemm_pair_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -907,7 +994,8 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_pair_kernel(const __grid_cons
       pair_tile_mn((NG == 1 || tile < split) ? tile : tile - split, e, tm, tn);
       const int row = tm * 2 * BM + (int)rank * BM + row_in_tile;
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
-      for (int c = 0; c < BN * NW / 32; ++c) {
+      if constexpr (EPI != 0) softmax_piece<EPI == 2>(p.sp, row, e.M, e.N, tn * BN, taddr);
+      else for (int c = 0; c < BN * NW / 32; ++c) {
         uint32_t r[32];
         tmem_ld32(taddr + (uint32_t)(c * 32), r);
         const int col = tn * BN * NW + c * 32;
@@ -986,7 +1074,10 @@ void init_once() {
                                 (const void*)gemm_pair_kernel<1, false, true, false, false, 2>,
                                 (const void*)gemm_pair_kernel<1, true, false, false, false, 2>,
                                 (const void*)gemm_pair_kernel<1, true, true, false, false, 2>,
-                                (const void*)gemm_pair_kernel<2, true, true, false, true, 2>};
+                                (const void*)gemm_pair_kernel<2, true, true, false, true, 2>,
+                                (const void*)gemm_pair_kernel<2, false, true, true, true>,
+                                (const void*)gemm_pair_kernel<1, false, false, false, false, 1, 1>,
+                                (const void*)gemm_pair_kernel<1, false, false, false, false, 1, 2>};
   for (const void* k : pair_kernels) {
     const cudaError_t a = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM_BYTES);
     if (a != cudaSuccess) g_init_err = a;
@@ -1115,7 +1206,7 @@ int pair_band(int K, int pairs) {
   return best;
 }
 
-template <int NG, bool A0, bool B0, bool A1, bool B1, int NW = 1>
+template <int NG, bool A0, bool B0, bool A1, bool B1, int NW = 1, int EPI = 0>
 cudaError_t launch_pair_kernel(const Params& p, int tiles, cudaStream_t s) {
   const int clusters = tiles < g_pair_clusters ? tiles : g_pair_clusters;
   cudaLaunchConfig_t cfg{};
@@ -1130,7 +1221,7 @@ cudaError_t launch_pair_kernel(const Params& p, int tiles, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<NG, A0, B0, A1, B1, NW>, p);
+  return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<NG, A0, B0, A1, B1, NW, EPI>, p);
 }
 
 cudaError_t launch(const GemmArgs* gs, int n, cudaStream_t s) {
@@ -1280,6 +1371,66 @@ cudaError_t gemm_pair(const GemmArgs& g0, const GemmArgs& g1, cudaStream_t s) {
   }
   cudaError_t e = launch(&g0, 1, s);
   return e != cudaSuccess ? e : launch(&g1, 1, s);
+}
+
+cudaError_t gemm_softmax_pieces(const bf16* A, const bf16* B, int M, int N, int K, const SoftmaxPieces& sp,
+                                int* tile_ctr, cudaStream_t s) {
+  std::call_once(g_once, init_once);
+  if (g_init_err != cudaSuccess) return g_init_err;
+  if (M <= 0 || N <= 0 || K <= 0 || K % 8 || !al16(A) || !al16(B) || !sp.stat || !sp.zt || !sp.target || !tile_ctr)
+    return cudaErrorInvalidValue;
+  if (sp.npieces != (N + BN - 1) / BN || (sp.E && (!al16(sp.E) || sp.ldE % 8 || sp.ldE < N))) return cudaErrorInvalidValue;
+  Params p;
+  std::memset(&p, 0, sizeof p);
+  if (!make_map(&p.ta[0], A, M, K, K, BM) || !make_map(&p.tb[0], B, N, K, K, BN / 2)) return cudaErrorInvalidValue;
+  fill_epi(&p.e[0], M, N, K, nullptr, 0);
+  p.e[0].group_m = pair_band(K, g_pair_clusters);
+  p.ngroups = 1;
+  p.tile_start[1] = (M + 2 * BM - 1) / (2 * BM) * p.e[0].tiles_n;
+  p.tile_ctr = tile_ctr;
+  p.sp = sp;
+  p.stall = gemm_stall_take();
+  const cudaError_t r = sp.E ? launch_pair_kernel<1, false, false, false, false, 1, 2>(p, p.tile_start[1], s)
+                             : launch_pair_kernel<1, false, false, false, false, 1, 1>(p, p.tile_start[1], s);
+  return r != cudaSuccess ? r : cudaGetLastError();
+}
+
+cudaError_t gemm_grads(const GemmArgs& dgrad, const GemmArgs& wgrad, int* tile_ctr, cudaStream_t s) {
+  std::call_once(g_once, init_once);
+  if (g_init_err != cudaSuccess) return g_init_err;
+  const GemmArgs* gs[2] = {&dgrad, &wgrad};
+  if (!tile_ctr || dgrad.a_mn || !dgrad.b_mn || !wgrad.a_mn || !wgrad.b_mn) return cudaErrorInvalidValue;
+  Params p;
+  std::memset(&p, 0, sizeof p);
+  p.ngroups = 2;
+  for (int i = 0; i < 2; ++i) {
+    const cudaError_t e = fill_group(*gs[i], &p.ta[i], &p.tb[i], &p.e[i], true);
+    if (e != cudaSuccess) return e;
+    p.e[i].group_m = pair_band(p.e[i].K, g_pair_clusters);
+    p.tile_start[i + 1] = p.tile_start[i] + (p.e[i].M + 2 * BM - 1) / (2 * BM) * p.e[i].tiles_n;
+  }
+  p.tile_ctr = tile_ctr;
+  p.stall = gemm_stall_take();
+  const cudaError_t r = launch_pair_kernel<2, false, true, true, true>(p, p.tile_start[2], s);
+  return r != cudaSuccess ? r : cudaGetLastError();
+}
+
+cudaError_t gemm_one(const GemmArgs& g, int* tile_ctr, cudaStream_t s) {
+  std::call_once(g_once, init_once);
+  if (g_init_err != cudaSuccess) return g_init_err;
+  if (!tile_ctr || !g.b_mn) return cudaErrorInvalidValue;
+  Params p;
+  std::memset(&p, 0, sizeof p);
+  p.ngroups = 1;
+  const cudaError_t e = fill_group(g, &p.ta[0], &p.tb[0], &p.e[0], true);
+  if (e != cudaSuccess) return e;
+  p.e[0].group_m = pair_band(g.K, g_pair_clusters);
+  p.tile_start[1] = (g.M + 2 * BM - 1) / (2 * BM) * p.e[0].tiles_n;
+  p.tile_ctr = tile_ctr;
+  p.stall = gemm_stall_take();
+  const cudaError_t r = g.a_mn ? launch_pair_kernel<1, true, true, false, false>(p, p.tile_start[1], s)
+                               : launch_pair_kernel<1, false, true, false, false>(p, p.tile_start[1], s);
+  return r != cudaSuccess ? r : cudaGetLastError();
 }
 
 cudaError_t kernel_error_read(int* code, int clear) {

@@ -60,6 +60,29 @@ struct GemmKGroupArgs {
   int ngrp; const int* grp_e; const int* grp_k0; const int* grp_klen;
 };
 cudaError_t gemm_expert_kgroups(const GemmKGroupArgs& g, cudaStream_t s);
+// Softmax statistics of logits Z = A B^T ([M][N], K-major operands with row
+// stride K) that are never written: per row and piece of 256 columns, (m, s) =
+// (largest logit, sum exp(z - m) without the target's column) from the FP32
+// accumulators; with E, also E[m, n] = bf16_rne(exp(z - m of its piece)), 0 at
+// the target; zt[r] = the logit of column target[r] (rows whose target is
+// outside [0, N) leave zt as it was).  K a
+// multiple of 8, A, B and E 16-byte aligned, ldE a multiple of 8.
+struct SoftmaxPieces {
+  float2* stat;           // [M][npieces]
+  int npieces;            // ceil(N / 256)
+  const int32_t* target;  // [M]
+  float* zt;              // [M]
+  bf16* E; int64_t ldE;   // null: statistics only
+};
+// tile_ctr: the launch's tile counter, zero on entry and left zero; the caller's
+// memory, so that launches of different callers share nothing.
+cudaError_t gemm_softmax_pieces(const bf16* A, const bf16* B, int M, int N, int K, const SoftmaxPieces& sp,
+                                int* tile_ctr, cudaStream_t s);
+// dX = dY W (a_mn = 0, b_mn = 1) and dW = dY^T X (a_mn = b_mn = 1) in one
+// launch with the caller's tile counter, the input gradient's tiles (the long
+// sums of an LM head) first; and either of them alone.
+cudaError_t gemm_grads(const GemmArgs& dgrad, const GemmArgs& wgrad, int* tile_ctr, cudaStream_t s);
+cudaError_t gemm_one(const GemmArgs& g, int* tile_ctr, cudaStream_t s);
 // Test hook: the next `launches` GEMM launches issue no loads, so their bounded
 // waits expire and they report through the kernel error word.
 void gemm_inject_stall(int launches);
@@ -120,6 +143,26 @@ cudaError_t reduce_sum(const float* x, int64_t n, float scale, float* out, cudaS
 cudaError_t f32_to_bf16_2d(const float* x, int64_t ldx, int64_t rows, int64_t cols, bf16* y,
                            int64_t ldy, float scale, cudaStream_t s);
 cudaError_t add_bf16(const bf16* a, const bf16* b, int64_t n, bf16* y, cudaStream_t s);
+
+// ---------------------------------------------------------------- losses (k_loss.cu)
+// The LM head and its cross-entropy without the logits: row_loss[t] = lse(h_t W^T)
+// - (h_t W^T)[target[t]]; dh and dW (either may be null) = gradients of g
+// sum_t row_loss[t].  Targets outside [0, V): zero loss and gradient.
+size_t linear_cross_entropy_scratch(int64_t T, int H, int V, bool grads);
+cudaError_t linear_cross_entropy(const bf16* h, const bf16* W, const int32_t* target, int64_t T, int H, int V, float g,
+                                 float* row_loss, bf16* dh, bf16* dW, void* scratch, size_t scratch_bytes,
+                                 cudaStream_t s);
+// Distillation from a teacher's K largest logits per row, with optional hard
+// targets; dlogits (null: losses only) may be logits itself.
+cudaError_t distill_topk(const bf16* logits, const int32_t* target, const float* t_val, const int32_t* t_idx,
+                         int64_t rows, int V, int K, float tau, float w_ce, float w_kd, float* row_ce, float* row_kd,
+                         bf16* dlogits, cudaStream_t s);
+// Balance and z loss of a router over groups of S tokens, per-expert counts and
+// mean probabilities, gradient of the router logits (null: losses only).
+size_t router_balance_scratch(int64_t T, int S, int E);
+cudaError_t router_balance(const float* logits, const int32_t* idx, const uint8_t* valid, int64_t T, int S, int E,
+                           int k, float alpha, float z_coef, float* loss, int32_t* counts, float* prob, bf16* dlogits,
+                           void* scratch, size_t scratch_bytes, cudaStream_t s);
 
 // ---------------------------------------------------------------- debug guards
 // bad[0] = the lowest index g < n whose 4096 bytes at base + offs[g] are not

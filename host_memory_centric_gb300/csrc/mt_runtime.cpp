@@ -2562,6 +2562,36 @@ mt_status mt_cross_entropy(void* logits, const int32_t* target, int64_t rows, in
   return cu_status(mt::cross_entropy((bf16*)logits, target, rows, V, inv_norm, row_loss, (cudaStream_t)stream));
 }
 
+size_t mt_linear_cross_entropy_scratch_bytes(int64_t T, int32_t H, int32_t V, int32_t grads) {
+  return mt::linear_cross_entropy_scratch(T, H, V, grads != 0);
+}
+
+mt_status mt_linear_cross_entropy(const void* h, const void* W, const int32_t* target, int64_t T, int32_t H, int32_t V,
+                                  float inv_norm, float* row_loss, void* dh, void* dW, void* scratch,
+                                  size_t scratch_bytes, void* stream) {
+  if (!h || !W || !target || !row_loss || !scratch) return MT_ERR_ARG;
+  return cu_status(mt::linear_cross_entropy((const bf16*)h, (const bf16*)W, target, T, H, V, inv_norm, row_loss,
+                                            (bf16*)dh, (bf16*)dW, scratch, scratch_bytes, (cudaStream_t)stream));
+}
+
+mt_status mt_distill_topk(const void* logits, const int32_t* target, const float* t_val, const int32_t* t_idx,
+                          int64_t rows, int32_t V, int32_t K, float tau, float w_ce, float w_kd, float* row_ce,
+                          float* row_kd, void* dlogits, void* stream) {
+  if (!logits || !t_val || !t_idx || !row_kd || (row_ce && !target)) return MT_ERR_ARG;
+  return cu_status(mt::distill_topk((const bf16*)logits, target, t_val, t_idx, rows, V, K, tau, w_ce, w_kd, row_ce,
+                                    row_kd, (bf16*)dlogits, (cudaStream_t)stream));
+}
+
+size_t mt_router_balance_scratch_bytes(int64_t T, int32_t S, int32_t E) { return mt::router_balance_scratch(T, S, E); }
+
+mt_status mt_router_balance(const float* logits, const int32_t* idx, const uint8_t* valid, int64_t T, int32_t S,
+                            int32_t E, int32_t k, float alpha, float z_coef, float* loss, int32_t* counts, float* prob,
+                            void* dlogits, void* scratch, size_t scratch_bytes, void* stream) {
+  if (!logits || !idx || !loss || !counts || !prob || !scratch) return MT_ERR_ARG;
+  return cu_status(mt::router_balance(logits, idx, valid, T, S, E, k, alpha, z_coef, loss, counts, prob,
+                                      (bf16*)dlogits, scratch, scratch_bytes, (cudaStream_t)stream));
+}
+
 size_t mt_moe_scratch_bytes(int64_t T, int32_t H, int32_t E, int32_t k, int32_t Fe) {
   if (T < 0 || H <= 0 || E <= 0 || k <= 0 || Fe <= 0) return 0;
   MoeWs w;

@@ -140,6 +140,88 @@ def cross_entropy(logits, target, inv_norm, row_loss):
     _chk(_L().mt_cross_entropy(_p(logits), _p(target), rows, V, inv_norm, _p(row_loss), _stream()))
 
 
+def _want(name, t, dtype, shape, optional=False):
+    """Refuses a tensor the library would misread: another type, shape, stride or device."""
+    from . import MtError
+    if t is None:
+        if optional:
+            return
+        raise MtError(-1, f"{name} is missing")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise MtError(-1, f"{name}: want a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                          f"{tuple(t.shape)} with strides {t.stride()}")
+    import torch
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise MtError(-1, f"{name} is on {t.device}, not on the current CUDA device")
+
+
+def _want_scratch(scratch, nbytes):
+    from . import MtError
+    if scratch is None or not scratch.is_contiguous() or scratch.device.type != "cuda" \
+            or scratch.numel() * scratch.element_size() < nbytes:
+        raise MtError(-1, f"scratch: want {nbytes} bytes of contiguous device memory")
+
+
+def linear_cross_entropy_scratch_bytes(T, H, V, grads=True) -> int:
+    return int(_L().mt_linear_cross_entropy_scratch_bytes(T, H, V, int(grads)))
+
+
+def linear_cross_entropy(h, W, target, inv_norm, row_loss, dh, dW, scratch):
+    """LM head and cross-entropy without the logits (mt_linear_cross_entropy):
+    row_loss [T] of h [T, H] against W [V, H], and the gradients dh and dW of
+    inv_norm * row_loss.sum() (None: not computed)."""
+    import torch
+    bf = torch.bfloat16
+    T, H = h.shape
+    V = W.shape[0]
+    _want("h", h, bf, (T, H)); _want("W", W, bf, (V, H)); _want("target", target, torch.int32, (T,))
+    _want("row_loss", row_loss, torch.float32, (T,))
+    _want("dh", dh, bf, (T, H), True); _want("dW", dW, bf, (V, H), True)
+    grads = dh is not None or dW is not None
+    _want_scratch(scratch, linear_cross_entropy_scratch_bytes(T, H, V, grads))
+    _chk(_L().mt_linear_cross_entropy(_p(h), _p(W), _p(target), T, H, V, inv_norm, _p(row_loss), _p(dh), _p(dW),
+                                      _p(scratch), scratch.numel() * scratch.element_size(), _stream()))
+
+
+def distill_topk(logits, target, t_val, t_idx, tau, w_ce, w_kd, row_ce, row_kd, dlogits):
+    """Distillation from a teacher's top logits (mt_distill_topk).  target and
+    row_ce may be None (no hard targets), dlogits None (losses only) or logits
+    itself."""
+    import torch
+    rows, V = logits.shape
+    K = t_val.shape[1]
+    _want("logits", logits, torch.bfloat16, (rows, V)); _want("target", target, torch.int32, (rows,), True)
+    _want("t_val", t_val, torch.float32, (rows, K)); _want("t_idx", t_idx, torch.int32, (rows, K))
+    _want("row_ce", row_ce, torch.float32, (rows,), True); _want("row_kd", row_kd, torch.float32, (rows,))
+    _want("dlogits", dlogits, torch.bfloat16, (rows, V), True)
+    _chk(_L().mt_distill_topk(_p(logits), _p(target), _p(t_val), _p(t_idx), rows, V, K, tau, w_ce, w_kd, _p(row_ce),
+                              _p(row_kd), _p(dlogits), _stream()))
+
+
+def router_balance_scratch_bytes(T, S, E) -> int:
+    return int(_L().mt_router_balance_scratch_bytes(T, S, E))
+
+
+def router_balance(logits, idx, valid, S, alpha, z_coef, loss, counts, prob, dlogits, scratch):
+    """Balance and z loss of a router over groups of S tokens, counts and mean
+    probabilities per group and expert, gradient of the logits
+    (mt_router_balance).  valid and dlogits may be None."""
+    import torch
+    from . import MtError
+    T, E = logits.shape
+    k = idx.shape[1]
+    if S < 1 or T % S:
+        raise MtError(-1, f"{T} tokens are not groups of {S}")
+    _want("logits", logits, torch.float32, (T, E)); _want("idx", idx, torch.int32, (T, k))
+    _want("valid", valid, torch.uint8, (T,), True); _want("loss", loss, torch.float32, (2,))
+    _want("counts", counts, torch.int32, (T // S, E)); _want("prob", prob, torch.float32, (T // S, E))
+    _want("dlogits", dlogits, torch.bfloat16, (T, E), True)
+    _want_scratch(scratch, router_balance_scratch_bytes(T, S, E))
+    _chk(_L().mt_router_balance(_p(logits), _p(idx), _p(valid), T, S, E, k, alpha, z_coef, _p(loss), _p(counts),
+                                _p(prob), _p(dlogits), _p(scratch), scratch.numel() * scratch.element_size(),
+                                _stream()))
+
+
 def moe_scratch_bytes(T, H, E, k, Fe):
     return int(_L().mt_moe_scratch_bytes(T, H, E, k, Fe))
 

@@ -446,6 +446,63 @@ mt_status mt_embed_bwd(const int32_t* row_start, const int32_t* rows, const void
  * target (zero gradient, zero loss); row_loss[r] = lse - logit[target]. */
 mt_status mt_cross_entropy(void* logits, const int32_t* target, int64_t rows, int32_t V,
                            float inv_norm, float* row_loss, void* stream);
+/* The LM head and its cross-entropy in one call, without the logits: with
+ * z = h W^T (h [T][H], W [V][H] BF16), row_loss[t] = lse(z_t) - z_t[target[t]]
+ * (FP32, from the FP32 products) and, for inv_norm * sum_t row_loss[t], the
+ * gradients dh ([T][H] BF16) and dW ([V][H] BF16, every row written); dh, dW
+ * or both may be null and are then not computed.  A target outside [0, V)
+ * marks a row with no target (zero loss, no gradient).  The softmax is taken
+ * in pieces of 256 columns as the product's tiles come out; for the gradients
+ * the exponentials of a bounded chunk of tokens (about 1 GiB) are held in
+ * BF16, relative to each piece's maximum, so their error does not grow with
+ * the logits; over several chunks dW is summed in FP32.  scratch: 256-byte
+ * aligned device memory of
+ * mt_linear_cross_entropy_scratch_bytes(T, H, V, dh or dW wanted) bytes, not
+ * shared by calls that may overlap.  H a multiple of 8, V <= 2097152, h, W, dh
+ * and dW 16-byte aligned, else MT_ERR_ARG.  T = 0 writes nothing.  No host
+ * synchronisation; may be captured into a graph. */
+size_t mt_linear_cross_entropy_scratch_bytes(int64_t T, int32_t H, int32_t V, int32_t grads);
+mt_status mt_linear_cross_entropy(const void* h, const void* W, const int32_t* target, int64_t T, int32_t H, int32_t V,
+                                  float inv_norm, float* row_loss, void* dh, void* dW, void* scratch,
+                                  size_t scratch_bytes, void* stream);
+/* Distillation from a teacher's top logits, with optional hard targets, per
+ * row of student logits z ([rows][V] BF16): the teacher's K largest logits y
+ * ([rows][K] FP32) at the ids t_idx ([rows][K] int32; an id outside [0, V) is
+ * an empty slot).  With q = softmax over the filled slots of y / tau and
+ * p = softmax(z / tau),
+ *   row_kd = sum_j q_j (log q_j - log p[id_j])          (terms with q_j = 0 are 0)
+ *   row_ce = lse(z) - z[target]                          (target null: none)
+ *   dlogits = w_ce (softmax(z) - onehot(target)) + w_kd / tau (p - q at the ids)
+ * (BF16 [rows][V], the gradient of w_ce row_ce + w_kd row_kd; null: losses
+ * only; may be logits itself).  An id in several slots counts with the sum of
+ * its q.  A row with no filled slot (or none above -inf) has no teacher part,
+ * a target outside [0, V) no hard part; a row with neither gets zeros.
+ * row_ce may be null.  1 <= K <= 1024, tau and 1 / tau finite and > 0, logits and dlogits 16-byte
+ * aligned, else MT_ERR_ARG; V may be odd. */
+mt_status mt_distill_topk(const void* logits, const int32_t* target, const float* t_val, const int32_t* t_idx,
+                          int64_t rows, int32_t V, int32_t K, float tau, float w_ce, float w_kd, float* row_ce,
+                          float* row_kd, void* dlogits, void* stream);
+/* Auxiliary losses of a router and their gradient.  logits [T][E] FP32, idx
+ * [T][k] int32 (mt_moe_ffn's selection; values outside [0, E) are not
+ * counted), valid [T] uint8 (null: every token; 0 marks padding, which counts
+ * nowhere).  The tokens form G = T / S groups of S consecutive rows (a
+ * sequence each, or S = T); with n valid tokens in a group, counts[g][e] of
+ * its choices on expert e, f = counts / (n k) and prob[g][e] the mean over
+ * valid tokens of softmax(logits),
+ *   loss[0] = alpha E / G sum_g sum_e f prob         (load balance)
+ *   loss[1] = z_coef / G sum_g (mean over valid tokens of lse^2)
+ * dlogits ([T][E] BF16, null: losses only) is the gradient of their sum (f
+ * held constant), zero for padding; a group with no valid token adds nothing
+ * and has zero counts and prob.  To add it to mt_moe_ffn's gradients, multiply
+ * it with Wr and yn (mt_gemm).  scratch: 256-byte aligned device memory of
+ * mt_router_balance_scratch_bytes(T, S, E) bytes, not shared by calls that may
+ * overlap.  1 <= k <= E <= 512, S a divisor of T, at most 65535 groups, S k <
+ * 2^31, logits and dlogits 16-byte aligned, else MT_ERR_ARG.  T = 0 writes
+ * nothing. */
+size_t mt_router_balance_scratch_bytes(int64_t T, int32_t S, int32_t E);
+mt_status mt_router_balance(const float* logits, const int32_t* idx, const uint8_t* valid, int64_t T, int32_t S,
+                            int32_t E, int32_t k, float alpha, float z_coef, float* loss, int32_t* counts, float* prob,
+                            void* dlogits, void* scratch, size_t scratch_bytes, void* stream);
 /* Per-launch timing of the library's own kernels: CUDA events around each
  * launch on the compute stream.  kind 0 = GEMMs, 1 = attention forward,
  * 2 = attention backward, 3 = all other kernels.  mt_timing(model, 1) resets
