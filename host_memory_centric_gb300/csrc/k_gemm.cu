@@ -50,6 +50,7 @@
 // of A once for 512 output columns.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <cuda_fp16.h>
 
 #include <atomic>
 #include <cstring>
@@ -80,6 +81,12 @@ struct Epi {
   int M, N, K;
   int tiles_m, tiles_n, group_m;
   int a_mn, b_mn;
+  // gradient epilogue (EPI 3) only: D = bf16(alpha acc); with ksplit > 1 the K
+  // blocks are cut into ksplit runs of kb_per, run i's product going to
+  // Dacc + i * slab (FP32) instead
+  float alpha;
+  int ksplit, kb_per;
+  int64_t slab;
 };
 
 constexpr int MAX_EXPERT_GROUPS = 128;
@@ -226,6 +233,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -234,6 +246,7 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 
 // Epilogue of 32 consecutive columns of one output row.
+template <bool SCALED = false>
 __device__ __forceinline__ void epi_store(const Epi& e, int row, int col, const uint32_t (&r)[32]) {
   float v[32];
 #pragma unroll
@@ -267,6 +280,10 @@ __device__ __forceinline__ void epi_store(const Epi& e, int row, int col, const 
       }
     }
     if (e.D) {
+      if (SCALED) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= e.alpha;
+      }
       uint4* p = reinterpret_cast<uint4*>(e.D + (int64_t)row * e.ldd + col);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -282,7 +299,7 @@ __device__ __forceinline__ void epi_store(const Epi& e, int row, int col, const 
         *p = x;
       }
       if (e.R) x += __bfloat162float(e.R[(int64_t)row * e.ldr + col + i]);
-      if (e.D) e.D[(int64_t)row * e.ldd + col + i] = __float2bfloat16_rn(x);
+      if (e.D) e.D[(int64_t)row * e.ldd + col + i] = __float2bfloat16_rn(SCALED ? x * e.alpha : x);
     }
   }
 }
@@ -291,12 +308,13 @@ __device__ __forceinline__ void epi_store(const Epi& e, int row, int col, const 
 // col0 + 255 of N, in TMEM from taddr on): m = the row's largest logit of the
 // piece, s = sum exp(z - m) over its columns but the target's (which the join
 // adds from zt, so that 1 - p of a confident row is a sum and no difference),
-// both from the FP32 accumulators, to stat[row][piece]; e = bf16(exp(z - m)),
-// if wanted, to E; the target's logit, if it lies in the piece, to zt.  Two passes over the accumulator, since m has
-// to be known before the first exponential: reading TMEM twice costs less than
-// rescaling, and the epilogue hides behind the next tile's MMAs (at K = 3584 a
-// tile's MMAs take about 18 us, its epilogue about 3).  All lanes take part in
-// the loads; rows >= M store nothing.
+// both from the FP32 accumulators, to stat[row][piece]; the target's logit, if
+// it lies in the piece, to zt; if wanted, fp16(2^15 exp(z - m)) to E (11 bits
+// down to 20 nats below the piece's maximum; BF16 would round every gradient
+// element a second time as coarsely as the first).  Two passes over the
+// accumulator, since m has to be known before the first exponential: reading
+// TMEM twice costs less than rescaling, and the epilogue hides behind the next
+// tile's MMAs.  All lanes take part in the loads; rows >= M store nothing.
 template <bool STORE>
 __device__ __forceinline__ void softmax_piece(const SoftmaxPieces& sp, int row, int M, int N, int col0,
                                               uint32_t taddr) {
@@ -336,7 +354,7 @@ __device__ __forceinline__ void softmax_piece(const SoftmaxPieces& sp, int row, 
     // z - m first, exact for the terms that count, then the factor log2(e): a
     // fused z log2(e) - m log2(e) would lose digits where |z| is large
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = exp2_approx((__uint_as_float(r[i]) - ref) * kLog2e);
+    for (int i = 0; i < 32; ++i) v[i] = exp2_approx(fmaf(__uint_as_float(r[i]) - ref, kLog2e, 15.f));
     if (col + 32 > N) {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
@@ -357,11 +375,11 @@ __device__ __forceinline__ void softmax_piece(const SoftmaxPieces& sp, int row, 
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (col + 8 * i < N)  // ldE is N rounded up to 8 columns at least: a started vector fits the row
-          p[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                            pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+          p[i] = make_uint4(pack_half(v[8 * i], v[8 * i + 1]), pack_half(v[8 * i + 2], v[8 * i + 3]),
+                            pack_half(v[8 * i + 4], v[8 * i + 5]), pack_half(v[8 * i + 6], v[8 * i + 7]));
     }
   }
-  if (live) sp.stat[(int64_t)row * sp.npieces + col0 / BN] = make_float2(ref, s0 + s1);
+  if (live) sp.stat[(int64_t)row * sp.npieces + col0 / BN] = make_float2(ref, (s0 + s1) * 0x1p-15f);
 }
 
 // Producer side of one output tile: its K-blocks into the shared-memory ring.
@@ -713,7 +731,8 @@ template <bool A_MN, bool B_MN, int NW>
 __device__ __forceinline__ bool produce_pair_tile(const CUtensorMap* tmA, const CUtensorMap* tmB, int arow, int brow,
                                                   int nk, uint8_t* sA, uint8_t* sB, uint64_t* full, uint64_t* empty,
                                                   bool leader, int& stage, uint32_t& phase, volatile int* abort_flag,
-                                                  uint32_t& inflight_mask, uint32_t& inflight_parity) {
+                                                  uint32_t& inflight_mask, uint32_t& inflight_parity,
+                                                  int kb0 = 0) {
   for (int kb = 0; kb < nk; ++kb) {
     if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) return false;
     // the even CTA's full[stage] expects both CTAs' bytes
@@ -721,7 +740,7 @@ __device__ __forceinline__ bool produce_pair_tile(const CUtensorMap* tmA, const 
     const uint32_t bar = cluster_addr(&full[stage], 0);
     uint8_t* a = sA + stage * PA_BYTES;
     uint8_t* b = sB + stage * (NW * PB_BYTES);
-    const int k0 = kb * BK;
+    const int k0 = (kb0 + kb) * BK;
     if (!A_MN) {
       tma_load_pair(tmA, bar, a, k0, arow);
     } else {
@@ -807,8 +826,24 @@ __device__ __forceinline__ void st_cluster_s32(uint32_t addr, int v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// The K blocks of a tile of group `e`: all of them, or with EPI 3 one run of a
+// split sum, `tile` then becoming the tile's index within its run.
+template <int EPI>
+__device__ __forceinline__ void tile_run(const Epi& e, int& tile, int& run, int& kb0, int& nk) {
+  nk = (e.K + BK - 1) / BK;
+  run = kb0 = 0;
+  if (EPI == 3 && e.ksplit > 1) {
+    const int per = (e.M + 2 * BM - 1) / (2 * BM) * e.tiles_n;
+    run = tile / per;
+    tile -= run * per;
+    kb0 = run * e.kb_per;
+    nk = min(e.kb_per, nk - kb0);
+  }
+}
+
 // EPI 0: the plain epilogue (epi_store); 1 and 2: the softmax epilogue of a
-// narrow (256 x 256) tile, without and with the exponentials stored.
+// narrow (256 x 256) tile, without and with the exponentials stored; 3: the
+// plain epilogue with a factor, and split sums (Epi::alpha, ksplit).
 template <int NG, bool A0, bool B0, bool A1, bool B1, int NW = 1, int EPI = 0>
 __global__ void __launch_bounds__(THREADS, 1) gemm_pair_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -917,19 +952,20 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_pair_kernel(const __grid_cons
           mbar_arrive_remote(cluster_addr(&tid_empty[slot], 0));
         }
         if (tile < 0) break;
-        int tm, tn;
+        int tm, tn, run, kb0, nk;
         if (NG == 1 || tile < split) {
+          tile_run<EPI>(p.e[0], tile, run, kb0, nk);
           pair_tile_mn(tile, p.e[0], tm, tn);
           ok = produce_pair_tile<A0, B0, NW>(&p.ta[0], &p.tb[0], tm * 2 * BM + (int)rank * BM,
-                                             tn * BN * NW + (int)rank * (BN / 2),
-                                         (p.e[0].K + BK - 1) / BK, sA, sB, full, empty, leader, stage, phase,
-                                         abort_flag, inflight_mask, inflight_parity);
+                                             tn * BN * NW + (int)rank * (BN / 2), nk, sA, sB, full, empty, leader,
+                                             stage, phase, abort_flag, inflight_mask, inflight_parity, kb0);
         } else {
-          pair_tile_mn(tile - split, p.e[1], tm, tn);
+          tile -= split;
+          tile_run<EPI>(p.e[1], tile, run, kb0, nk);
+          pair_tile_mn(tile, p.e[1], tm, tn);
           ok = produce_pair_tile<A1, B1, NW>(&p.ta[1], &p.tb[1], tm * 2 * BM + (int)rank * BM,
-                                             tn * BN * NW + (int)rank * (BN / 2),
-                                         (p.e[1].K + BK - 1) / BK, sA, sB, full, empty, leader, stage, phase,
-                                         abort_flag, inflight_mask, inflight_parity);
+                                             tn * BN * NW + (int)rank * (BN / 2), nk, sA, sB, full, empty, leader,
+                                             stage, phase, abort_flag, inflight_mask, inflight_parity, kb0);
         }
       }
       if (!ok) fail(abort_flag, 1);
@@ -945,7 +981,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_pair_kernel(const __grid_cons
           ok = false;
           break;
         }
-        const int tile = tid_ring[slot];
+        int tile = tid_ring[slot];
         mbar_arrive(&tid_empty[slot]);
         if (tile < 0) break;
         // two 256-column accumulators, or one of 512 columns for wide tiles
@@ -957,10 +993,15 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_pair_kernel(const __grid_cons
         }
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(acc * BN);
-        if (NG == 1 || tile < split)
-          ok = mma_pair_tile<A0, B0, NW>(d, (p.e[0].K + BK - 1) / BK, sA, sB, full, empty, stage, phase, abort_flag);
-        else
-          ok = mma_pair_tile<A1, B1, NW>(d, (p.e[1].K + BK - 1) / BK, sA, sB, full, empty, stage, phase, abort_flag);
+        int run, kb0, nk;
+        if (NG == 1 || tile < split) {
+          tile_run<EPI>(p.e[0], tile, run, kb0, nk);
+          ok = mma_pair_tile<A0, B0, NW>(d, nk, sA, sB, full, empty, stage, phase, abort_flag);
+        } else {
+          tile -= split;
+          tile_run<EPI>(p.e[1], tile, run, kb0, nk);
+          ok = mma_pair_tile<A1, B1, NW>(d, nk, sA, sB, full, empty, stage, phase, abort_flag);
+        }
         if (!ok) break;
         tc_commit_pair(&tfull[acc]);  // both CTAs' epilogues may read their rows
       }
@@ -990,16 +1031,25 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_pair_kernel(const __grid_cons
       }
       tc_fence_after();
       const Epi& e = (NG == 1 || tile < split) ? p.e[0] : p.e[1];
-      int tm, tn;
-      pair_tile_mn((NG == 1 || tile < split) ? tile : tile - split, e, tm, tn);
+      int tm, tn, local = (NG == 1 || tile < split) ? tile : tile - split, run, kb0, nk;
+      tile_run<EPI>(e, local, run, kb0, nk);
+      pair_tile_mn(local, e, tm, tn);
+      Epi er;
+      if constexpr (EPI == 3) {
+        er = e;
+        if (e.ksplit > 1) er.Dacc += run * e.slab;
+      }
       const int row = tm * 2 * BM + (int)rank * BM + row_in_tile;
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
-      if constexpr (EPI != 0) softmax_piece<EPI == 2>(p.sp, row, e.M, e.N, tn * BN, taddr);
+      if constexpr (EPI == 1 || EPI == 2) softmax_piece<EPI == 2>(p.sp, row, e.M, e.N, tn * BN, taddr);
       else for (int c = 0; c < BN * NW / 32; ++c) {
         uint32_t r[32];
         tmem_ld32(taddr + (uint32_t)(c * 32), r);
         const int col = tn * BN * NW + c * 32;
-        if (row < e.M && col < e.N) epi_store(e, row, col, r);
+        if (row < e.M && col < e.N) {
+          if constexpr (EPI == 3) epi_store<true>(er, row, col, r);
+          else epi_store(e, row, col, r);
+        }
       }
       tc_fence_before();
       mbar_arrive_remote(tempty_lead[acc]);  // the even CTA counts both CTAs' epilogues
@@ -1075,7 +1125,9 @@ void init_once() {
                                 (const void*)gemm_pair_kernel<1, true, false, false, false, 2>,
                                 (const void*)gemm_pair_kernel<1, true, true, false, false, 2>,
                                 (const void*)gemm_pair_kernel<2, true, true, false, true, 2>,
-                                (const void*)gemm_pair_kernel<2, false, true, true, true>,
+                                (const void*)gemm_pair_kernel<2, false, true, true, true, 1, 3>,
+                                (const void*)gemm_pair_kernel<1, false, true, false, false, 1, 3>,
+                                (const void*)gemm_pair_kernel<1, true, true, false, false, 1, 3>,
                                 (const void*)gemm_pair_kernel<1, false, false, false, false, 1, 1>,
                                 (const void*)gemm_pair_kernel<1, false, false, false, false, 1, 2>};
   for (const void* k : pair_kernels) {
@@ -1395,41 +1447,47 @@ cudaError_t gemm_softmax_pieces(const bf16* A, const bf16* B, int M, int N, int 
   return r != cudaSuccess ? r : cudaGetLastError();
 }
 
-cudaError_t gemm_grads(const GemmArgs& dgrad, const GemmArgs& wgrad, int* tile_ctr, cudaStream_t s) {
+cudaError_t gemm_grads(const GradArgs& g, cudaStream_t s) {
   std::call_once(g_once, init_once);
   if (g_init_err != cudaSuccess) return g_init_err;
-  const GemmArgs* gs[2] = {&dgrad, &wgrad};
-  if (!tile_ctr || dgrad.a_mn || !dgrad.b_mn || !wgrad.a_mn || !wgrad.b_mn) return cudaErrorInvalidValue;
+  if (!g.tile_ctr || !(g.dgrad || g.wgrad) || (g.dgrad && (g.dgrad->a_mn || !g.dgrad->b_mn)) ||
+      (g.wgrad && (!g.wgrad->a_mn || !g.wgrad->b_mn)))
+    return cudaErrorInvalidValue;
   Params p;
   std::memset(&p, 0, sizeof p);
-  p.ngroups = 2;
-  for (int i = 0; i < 2; ++i) {
-    const cudaError_t e = fill_group(*gs[i], &p.ta[i], &p.tb[i], &p.e[i], true);
+  for (const GemmArgs* a : {g.dgrad, g.wgrad}) {
+    if (!a) continue;
+    const int i = p.ngroups++;
+    GemmArgs w = *a;
+    const bool split = a == g.dgrad && g.ksplit > 1;
+    if (split) {
+      if (!g.slabs) return cudaErrorInvalidValue;
+      w.D = nullptr;
+      w.Dacc = g.slabs;
+      w.ldacc = a->N;
+      w.acc_mode = 1;
+    }
+    const cudaError_t e = fill_group(w, &p.ta[i], &p.tb[i], &p.e[i], true);
     if (e != cudaSuccess) return e;
-    p.e[i].group_m = pair_band(p.e[i].K, g_pair_clusters);
-    p.tile_start[i + 1] = p.tile_start[i] + (p.e[i].M + 2 * BM - 1) / (2 * BM) * p.e[i].tiles_n;
+    Epi& ep = p.e[i];
+    ep.group_m = pair_band(ep.K, g_pair_clusters);
+    ep.alpha = g.alpha;
+    ep.ksplit = 1;
+    if (split) {  // as many runs as were asked for, or fewer if some would be empty
+      const int nk = (ep.K + BK - 1) / BK;
+      ep.kb_per = (nk + g.ksplit - 1) / g.ksplit;
+      ep.ksplit = (nk + ep.kb_per - 1) / ep.kb_per;
+      if (ep.ksplit != g.ksplit) return cudaErrorInvalidValue;
+      ep.slab = (int64_t)ep.M * ep.N;
+    }
+    p.tile_start[i + 1] = p.tile_start[i] + (ep.M + 2 * BM - 1) / (2 * BM) * ep.tiles_n * ep.ksplit;
   }
-  p.tile_ctr = tile_ctr;
+  p.tile_ctr = g.tile_ctr;
   p.stall = gemm_stall_take();
-  const cudaError_t r = launch_pair_kernel<2, false, true, true, true>(p, p.tile_start[2], s);
-  return r != cudaSuccess ? r : cudaGetLastError();
-}
-
-cudaError_t gemm_one(const GemmArgs& g, int* tile_ctr, cudaStream_t s) {
-  std::call_once(g_once, init_once);
-  if (g_init_err != cudaSuccess) return g_init_err;
-  if (!tile_ctr || !g.b_mn) return cudaErrorInvalidValue;
-  Params p;
-  std::memset(&p, 0, sizeof p);
-  p.ngroups = 1;
-  const cudaError_t e = fill_group(g, &p.ta[0], &p.tb[0], &p.e[0], true);
-  if (e != cudaSuccess) return e;
-  p.e[0].group_m = pair_band(g.K, g_pair_clusters);
-  p.tile_start[1] = (g.M + 2 * BM - 1) / (2 * BM) * p.e[0].tiles_n;
-  p.tile_ctr = tile_ctr;
-  p.stall = gemm_stall_take();
-  const cudaError_t r = g.a_mn ? launch_pair_kernel<1, true, true, false, false>(p, p.tile_start[1], s)
-                               : launch_pair_kernel<1, false, true, false, false>(p, p.tile_start[1], s);
+  const int tiles = p.tile_start[p.ngroups];
+  const cudaError_t r = p.ngroups == 2 ? launch_pair_kernel<2, false, true, true, true, 1, 3>(p, tiles, s)
+                        : g.dgrad      ? launch_pair_kernel<1, false, true, false, false, 1, 3>(p, tiles, s)
+                                       : launch_pair_kernel<1, true, true, false, false, 1, 3>(p, tiles, s);
   return r != cudaSuccess ? r : cudaGetLastError();
 }
 

@@ -7,6 +7,8 @@
 // of atomics, so the same inputs give the same bits.
 #include "mt_kernels.h"
 
+#include <cuda_fp16.h>
+
 namespace mt {
 namespace {
 
@@ -66,28 +68,33 @@ __device__ __forceinline__ float block_max(float v, float* red) {
 // target out, with M = max m_p:
 //   rest = sum_p s_p exp(m_p - M),  S = rest + exp(z_target - M),
 //   loss = (M - z_target) + log S,
-// and, with E, turns the stored exp(z - m_p) into the logits' gradient in
-// place: d = E exp(m_p - M) / S g, one factor per piece of 256 columns, and
-// d = -rest / S g (= (p - 1) g) at the target, so that loss and gradient of a
-// confident row (p near 1) keep their digits.  Rows without a target get zeros.
+// and, with E, turns the stored fp16 2^15 exp(z - m_p) into the logits'
+// gradient in BF16 in place: d = exp(z - m_p) exp(m_p - M) / S, one factor per
+// piece of 256 columns, and d = -rest / S (= p - 1) at the target, so that loss
+// and gradient of a confident row (p near 1) keep their digits.  The factor g
+// of the gradients waits for the products' FP32 results: rounded here, g (p - 1)
+// of most rows would be off by the same amount, and the errors would add up.
+// Rows without a target get zeros.  Bound by HBM (4 bytes a logit).  The blocks
+// of grid.y share a row; each joins the statistics for itself.
 constexpr int JOIN_THREADS = 256;
 
 __global__ void __launch_bounds__(JOIN_THREADS) ce_join_k(const float2* __restrict__ stat, int npieces,
                                                           const int32_t* __restrict__ target,
-                                                          const float* __restrict__ zt, int V, float g,
-                                                          float* __restrict__ row_loss, bf16* __restrict__ E,
+                                                          const float* __restrict__ zt, int V,
+                                                          float* __restrict__ row_loss, uint16_t* __restrict__ E,
                                                           int64_t ldE) {
-  extern __shared__ float f[];  // [npieces]
   __shared__ float red[JOIN_THREADS / 32];
   const int64_t row = blockIdx.x;
   const int tgt = target[row];
   const bool has = tgt >= 0 && tgt < V;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint4* e = reinterpret_cast<uint4*>(E + row * ldE);
+  const int nvec = (V + 7) / 8, step = 32 * (JOIN_THREADS / 32) * (int)gridDim.y;
+  const int first = ((int)blockIdx.y * (JOIN_THREADS / 32) + warp) * 32 + lane;  // a warp's 32 vectors are one piece
   if (!has) {
-    if (threadIdx.x == 0) row_loss[row] = 0.f;
+    if (threadIdx.x == 0 && blockIdx.y == 0) row_loss[row] = 0.f;
     if (E)
-      for (int64_t c = threadIdx.x * 8; c < V; c += JOIN_THREADS * 8)
-        *reinterpret_cast<uint4*>(E + row * ldE + c) = make_uint4(0, 0, 0, 0);
+      for (int v = first; v < nvec; v += step) e[v] = make_uint4(0, 0, 0, 0);
     return;
   }
   const float2* st = stat + row * npieces;
@@ -98,132 +105,355 @@ __global__ void __launch_bounds__(JOIN_THREADS) ce_join_k(const float2* __restri
   for (int p = threadIdx.x; p < npieces; p += JOIN_THREADS) s += st[p].y * expf(st[p].x - M);
   const float rest = block_sum<JOIN_THREADS>(s, red);
   const float z = zt[row], et = expf(z - M), S = rest + et;
-  if (threadIdx.x == 0) row_loss[row] = z == M ? log1pf(rest) : (M - z) + logf(S);
+  if (threadIdx.x == 0 && blockIdx.y == 0) row_loss[row] = z == M ? log1pf(rest) : (M - z) + logf(S);
   if (!E) return;
-  for (int p = threadIdx.x; p < npieces; p += JOIN_THREADS) f[p] = expf(st[p].x - M) / S * g;
-  __syncthreads();
-  const float dt = -rest / S * g;
-  bf16* e = E + row * ldE;
-  for (int p = warp; p < npieces; p += JOIN_THREADS / 32) {  // a warp's 32 vectors are one piece
-    const int c = p * 256 + lane * 8;
-    if (c >= V) continue;
-    float v[8];
-    unpack8(*reinterpret_cast<const uint4*>(e + c), v);
+  const float scale = 0x1p-15f / S, dt = -rest / S;
+  constexpr int U = 4;  // vectors of a thread on their way at a time
+  for (int v = first; v < nvec; v += U * step) {
+    uint4 q[U];
+    float f[U];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = c + k == tgt ? dt : v[k] * f[p];
-    *reinterpret_cast<uint4*>(e + c) = pack8(v);
+    for (int u = 0; u < U; ++u) {
+      const int w = v + u * step;
+      if (w < nvec) {
+        q[u] = e[w];
+        f[u] = st[w >> 5].x;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int w = v + u * step;
+      if (w >= nvec) continue;
+      const float k = expf(f[u] - M) * scale;
+      const __half2* h = reinterpret_cast<const __half2*>(&q[u]);
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 t = __half22float2(h[i]);
+        x[2 * i] = t.x * k;
+        x[2 * i + 1] = t.y * k;
+      }
+      if (w == tgt >> 3) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (w * 8 + i == tgt) x[i] = dt;
+      }
+      e[w] = pack8(x);
+    }
   }
 }
 
+// dh = bf16(g sum over the runs of a split sum), n4 groups of four values.
+__global__ void __launch_bounds__(256) ce_add_runs_k(const float4* __restrict__ slabs, int64_t n4, int runs, float g,
+                                                     uint2* __restrict__ dh) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int r = 0; r < runs; ++r) {
+    const float4 u = slabs[r * n4 + i];
+    v.x += u.x;
+    v.y += u.y;
+    v.z += u.z;
+    v.w += u.w;
+  }
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * g, v.y * g), b = __floats2bfloat162_rn(v.z * g, v.w * g);
+  dh[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// ------------------------------------------------------------------ cluster helpers
+__device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// shared::cluster address of the object at the same offset in CTA `rank`
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(su32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+// A kernel launched with programmatic serialisation may start while the one
+// before it runs; it sees that one's writes after dep_wait().
+__device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // ------------------------------------------------------------------ distillation
-// One block per row of student logits z, teacher logits y at ids i:
+// A row of student logits z, teacher logits y at ids i:
 //   q = softmax over the filled slots of y / tau, p = softmax(z / tau),
 //   kd = sum_j q_j (log q_j - log p_{i_j}),  ce = lse(z) - z_target,
 //   dz_v = w_ce (softmax(z)_v - [v = target]) + w_kd / tau (p_v - sum_{i_j = v} q_j).
-// The row is read twice (the second time from L2): statistics at both
-// temperatures, then the dense part of the gradient; the at most K + 1 columns
-// with a teacher entry or the target are then written again from their logits
-// kept in FP32, each by one thread, so that no element is rounded twice and an
-// id that appears in several slots gets the sum of their q.
-constexpr int KD_THREADS = 512;
+// Bound by HBM: the row has to be known before its first gradient element, so
+// it is read once and kept: a cluster of 1 to 8 blocks holds a row in
+// registers, NV 16-byte vectors a thread, all of them loaded before the first
+// is used.  Every thread sums exp(z - m) around its own maximum m at both
+// temperatures; each warp sends its joined (m, s1, st) to every block of the
+// cluster through distributed shared memory, and after the one barrier every
+// warp joins them all; then the gradient is computed from the same registers.
+// The last warp of a block holds no part of the row: it works out the
+// teacher's distribution, whose dependent loads would otherwise stand before
+// the barrier.  The at most K + 1 columns with a teacher entry or the target
+// are written again from their FP32 values by the block that holds them, each
+// by one thread, so that no element is rounded twice and an id that appears in
+// several slots gets the sum of their q, in slot order.
 constexpr int KD_MAX_K = 1024;
+constexpr int KD_MAX_CLUSTER = 8;
+constexpr int KD_WIDE_NV = 18;
+constexpr int KD_MAX_V = 524288;
+static_assert(KD_MAX_CLUSTER * 480 * KD_WIDE_NV * 8 >= KD_MAX_V, "the widest form holds the widest row");
 
-struct RunningSum {  // sum of exp(a (z - m)) at two scales a around one running maximum m
-  float m = -INFINITY, s1 = 0.f, st = 0.f;
-  __device__ __forceinline__ void add(float z, float it) {
-    if (z > m) {
-      s1 = m == -INFINITY ? 1.f : s1 * expf(m - z) + 1.f;
-      st = m == -INFINITY ? 1.f : st * expf((m - z) * it) + 1.f;
-      m = z;
-    } else if (m != -INFINITY || z != z) {
-      s1 += expf(z - m);
-      st += expf((z - m) * it);
-    }
-  }
+struct KdArgs {
+  const bf16* logits;
+  const int32_t* target;
+  const float* t_val;
+  const int32_t* t_idx;
+  int V, K;
+  float tau, w_ce, w_kd;
+  float *row_ce, *row_kd;
+  bf16* dlogits;
 };
 
-__global__ void __launch_bounds__(KD_THREADS) distill_k(const bf16* logits, const int32_t* __restrict__ target,
-                                                        const float* __restrict__ t_val,
-                                                        const int32_t* __restrict__ t_idx, int V, int K, float tau,
-                                                        float w_ce, float w_kd, float* __restrict__ row_ce,
-                                                        float* __restrict__ row_kd, bf16* dlogits) {
-  __shared__ float red[KD_THREADS / 32];
-  __shared__ int id[KD_MAX_K];
-  __shared__ float y[KD_MAX_K], q[KD_MAX_K], zj[KD_MAX_K];
-  const int64_t row = blockIdx.x;
-  const bf16* z = logits + row * V;
-  const float it = 1.f / tau;
-  const int tid = threadIdx.x;
-  const int tgt = target ? target[row] : -1;
+__device__ __forceinline__ uint32_t bf16_bits(const bf16* p) { return *reinterpret_cast<const uint16_t*>(p); }
+
+// Blocks per SM that the registers are to allow: the row's 4 NV and about 36
+// more a thread, else the compiler keeps unpacked copies of the row (254 registers at NV = 12).
+template <int NV, int NT>
+constexpr int kd_blocks() {
+  return 65536 / (NT * (4 * NV + 36)) > 6 ? 6 : 65536 / (NT * (4 * NV + 36));
+}
+template <int NV, int NT>
+__global__ void __launch_bounds__(NT, kd_blocks<NV, NT>()) distill_k(const KdArgs a) {
+  constexpr int DT = NT - 32, DW = DT / 32;  // threads and warps that hold the row
+  extern __shared__ __align__(16) float slots[];  // id [K4], y / tau - max [K4], q [K4], z at id [K4]; K4 = K up to 4s
+  __shared__ float peer[KD_MAX_CLUSTER * DW][3];
+  __shared__ float t_sum;                    // sum of the teacher's exponentials; 0: no teacher
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int V = a.V, K = a.K, K4 = (K + 3) & ~3;
+  int* id = reinterpret_cast<int*>(slots);
+  float *y = slots + K4, *q = slots + 2 * K4, *zj = slots + 3 * K4;
+  const uint32_t rank = cluster_rank(), ncta = cluster_size();
+  const int64_t row = blockIdx.x / ncta;
+  const bf16* z = a.logits + row * V;
+  // 16-byte vectors of memory that the row touches; the first and last may hold
+  // elements of its neighbours, which are neither read nor written
+  const int skip = (int)((row * V) & 7);
+  const int nvec = (skip + V + 7) >> 3, per = (nvec + (int)ncta - 1) / (int)ncta;
+  const int v0 = (int)rank * per, v1 = min(nvec, v0 + per);
+  const float it = 1.f / a.tau, itl = it * kLog2e;
+  const int tgt = a.target ? a.target[row] : -1;
   const bool hard = tgt >= 0 && tgt < V;
-  const float zt = hard ? __bfloat162float(z[tgt]) : 0.f;
-  float ym = -INFINITY;
-  for (int j = tid; j < K; j += KD_THREADS) {
-    const int i = t_idx[row * K + j];
-    const bool in = i >= 0 && i < V;
-    const float v = in ? t_val[row * K + j] * it : -INFINITY;
-    id[j] = in ? i : -1;
-    y[j] = v;
-    zj[j] = in ? __bfloat162float(z[i]) : 0.f;
-    ym = fmaxf(ym, v);
-  }
-  ym = block_max<KD_THREADS>(ym, red);
-  const bool soft = ym != -INFINITY;
-  float ys = 0.f;
-  for (int j = tid; j < K; j += KD_THREADS) {
-    const float v = id[j] < 0 || !soft ? 0.f : expf(y[j] - ym);
-    q[j] = v;
-    ys += v;
-  }
-  ys = block_sum<KD_THREADS>(ys, red);
-  const float yl = logf(ys);
+  // one exponential where one temperature is needed or both are the same
+  const bool two = hard && a.tau != 1.f;
+  const uint4* zv = reinterpret_cast<const uint4*>(z - skip);
+  uint4 r[NV];
+  float zt = 0.f;
 
-  RunningSum r;
-  for (int c = tid; c < V; c += KD_THREADS) r.add(__bfloat162float(z[c]), it);
-  const float m = block_max<KD_THREADS>(r.m, red);
-  const float f1 = r.m == -INFINITY ? 0.f : expf(r.m - m), ft = r.m == -INFINITY ? 0.f : expf((r.m - m) * it);
-  // log p = (z - m) / tau - log sum exp((z - m) / tau): differences first, so
-  // that the size of the logits costs no digits
-  const float l1 = logf(block_sum<KD_THREADS>(r.s1 * f1, red));
-  const float lt = logf(block_sum<KD_THREADS>(r.st * ft, red));
+  if (warp < DW) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int v = v0 + j * DT + tid, c = v * 8 - skip;
+      r[j] = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);  // -inf: no probability
+      if (v < v1) {
+        if (c >= 0 && c + 8 <= V) {
+          r[j] = zv[v];
+        } else {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int e = c + 2 * k;
+            const uint32_t lo = e >= 0 && e < V ? bf16_bits(z + e) : 0xFF80u;
+            const uint32_t hi = e + 1 >= 0 && e + 1 < V ? bf16_bits(z + e + 1) : 0xFF80u;
+            w[k] = lo | (hi << 16);
+          }
+          r[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+    if (hard) zt = __bfloat162float(z[tgt]);
+    // packed maxima: exact, and NaN passes by (it shows in the sums)
+    __nv_bfloat162 mx = __halves2bfloat162(__ushort_as_bfloat16(0xFF80), __ushort_as_bfloat16(0xFF80));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r[j]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mx = __hmax2(mx, h[k]);
+    }
+    const float tm = fmaxf(__low2float(mx), __high2float(mx));
+    const float ref = tm == -INFINITY ? 0.f : tm;
+    float s1 = 0.f, st = 0.f;
+    if (two) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float f[8];
+        unpack8(r[j], f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float x = f[k] - ref;
+          s1 += ex2(x * kLog2e);
+          st += ex2(x * itl);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float f[8];
+        unpack8(r[j], f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) st += ex2((f[k] - ref) * itl);
+      }
+      s1 = st;
+    }
+    const float wm = warp_max(tm);
+    const float w1 = wm == -INFINITY ? 1.f : ex2((tm - wm) * kLog2e), wt = wm == -INFINITY ? 1.f : ex2((tm - wm) * itl);
+    s1 = warp_sum(s1 * w1);
+    st = warp_sum(st * wt);
+    if (lane < (int)ncta) {
+      const uint32_t to = cluster_addr(&peer[rank * DW + warp][0], (uint32_t)lane);
+      st_cluster(to, wm);
+      st_cluster(to + 4, s1);
+      st_cluster(to + 8, st);
+    }
+  } else {
+    // the teacher's distribution; every block of the cluster needs it for its own columns
+    if (hard) zt = __bfloat162float(z[tgt]);
+    float ym = -INFINITY;
+    bool nan = false;
+#pragma unroll 4
+    for (int j = lane; j < K4; j += 32) {
+      const int i = j < K ? a.t_idx[row * K + j] : -1;
+      const bool in = i >= 0 && i < V;
+      const float v = in ? a.t_val[row * K + j] * it : -INFINITY;
+      id[j] = in ? i : -1;
+      y[j] = v;
+      zj[j] = in ? __bfloat162float(z[i]) : 0.f;
+      ym = fmaxf(ym, v);
+      nan |= v != v;
+    }
+    ym = warp_max(ym);
+    nan = __any_sync(0xffffffffu, nan);
+    if (nan && ym == -INFINITY) ym = 0.f;  // a NaN among the slots shows in the row, it does not empty it
+    __syncwarp();
+    const bool some = ym != -INFINITY;
+    float ys = 0.f;
+    for (int j = lane; j < K4; j += 32) {
+      const float d = y[j] - ym, v = id[j] < 0 || !some ? 0.f : expf(d);
+      y[j] = d;
+      q[j] = v;
+      ys += v;
+    }
+    ys = warp_sum(ys);
+    __syncwarp();
+    if (some)
+      for (int j = lane; j < K4; j += 32) q[j] = id[j] < 0 ? 0.f : q[j] / ys;
+    if (lane == 0) t_sum = some ? ys : 0.f;
+  }
+  cluster_sync();  // also: every read of the row by this cluster is done before its first write (in place)
 
-  float kd = 0.f;
-  for (int j = tid; j < K; j += KD_THREADS) {
-    if (id[j] < 0 || !soft || q[j] == 0.f) continue;
-    q[j] /= ys;
-    kd += q[j] * ((y[j] - ym - yl) - ((zj[j] - m) * it - lt));
+  const int np = (int)ncta * DW;
+  float m = -INFINITY;
+  for (int i = lane; i < np; i += 32) m = fmaxf(m, peer[i][0]);
+  m = warp_max(m);
+  float s1 = 0.f, st = 0.f;
+  for (int i = lane; i < np; i += 32) {
+    const float d = peer[i][0] - m;
+    s1 += peer[i][1] * (m == -INFINITY ? 1.f : ex2(d * kLog2e));
+    st += peer[i][2] * (m == -INFINITY ? 1.f : ex2(d * itl));
   }
-  kd = block_sum<KD_THREADS>(kd, red);
-  if (tid == 0) {
-    row_kd[row] = soft ? kd : 0.f;
-    if (row_ce) row_ce[row] = hard ? l1 - (zt - m) : 0.f;
+  s1 = warp_sum(s1);
+  st = warp_sum(st);
+  const float ysum = t_sum;
+  const bool soft = !(ysum == 0.f);
+  // log p = (z - m) / tau - log S: differences first, so that the size of the logits costs no digits
+  const float l1 = logf(s1), lt = logf(st);
+  bf16* d = a.dlogits + row * V;
+  const float a1 = hard ? a.w_ce : 0.f, at = soft ? a.w_kd * it : 0.f;
+  if (warp == DW) {
+    if (rank == 0) {
+      float kd = 0.f;
+      const float yl = logf(ysum);
+      for (int j = lane; j < K; j += 32)
+        if (id[j] >= 0 && q[j] != 0.f) kd += q[j] * ((y[j] - yl) - ((zj[j] - m) * it - lt));
+      kd = warp_sum(kd);
+      if (lane == 0) {
+        a.row_kd[row] = soft ? kd : 0.f;
+        if (a.row_ce) a.row_ce[row] = hard ? l1 - (zt - m) : 0.f;
+      }
+    }
+  } else if (a.dlogits) {
+    uint4* dv = reinterpret_cast<uint4*>(d - skip);
+    const float c1 = hard ? a1 / s1 : 0.f, ct = soft ? at / st : 0.f, cs = two ? ct : c1 + ct;
+    const bool any = hard || soft;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int v = v0 + j * DT + tid, c = v * 8 - skip;
+      if (v >= v1) continue;
+      float f[8];
+      unpack8(r[j], f);
+      if (two) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float x = f[k] - m;
+          f[k] = c1 * ex2(x * kLog2e) + cs * ex2(x * itl);
+        }
+      } else if (any) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = cs * ex2((f[k] - m) * itl);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = 0.f;
+      }
+      if (c >= 0 && c + 8 <= V) {
+        dv[v] = pack8(f);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (c + k >= 0 && c + k < V) d[c + k] = __float2bfloat16_rn(f[k]);
+      }
+    }
   }
-  if (!dlogits) return;
-  bf16* d = dlogits + row * V;
-  const float a1 = hard ? w_ce : 0.f, at = soft ? w_kd * it : 0.f;
-  auto grad = [&](float x) {
-    float v = 0.f;
-    if (hard) v += a1 * expf((x - m) - l1);
-    if (soft) v += at * expf((x - m) * it - lt);
-    return v;
-  };
-  for (int c = tid; c < V; c += KD_THREADS) d[c] = __float2bfloat16_rn(grad(__bfloat162float(z[c])));
-  __syncthreads();
-  for (int j = tid; j <= K; j += KD_THREADS) {  // slot K: the target, if no slot names it
+  if (!a.dlogits) return;
+  __syncthreads();  // the dense part of this block's columns is written
+  const int e0 = v0 * 8 - skip, e1 = v1 * 8 - skip;
+  for (int j = tid; j <= K; j += NT) {  // slot K: the target, if no slot names it
     const int i = j < K ? id[j] : (hard ? tgt : -1);
-    if (i < 0 || (j < K && !soft && i != tgt)) continue;
+    if (i < 0 || i < e0 || i >= e1) continue;
     bool first = true;
     float qs = 0.f;
-    for (int u = 0; u < K; ++u) {
-      if (id[u] != i) continue;
-      if (u < j) first = false;
-      qs += q[u];
+    for (int u = 0; u < K4; u += 4) {
+      const int4 w = *reinterpret_cast<const int4*>(id + u);
+      if (w.x != i && w.y != i && w.z != i && w.w != i) continue;
+#pragma unroll 1
+      for (int k = u; k < u + 4; ++k) {
+        if (id[k] != i) continue;
+        if (k < j) first = false;
+        qs += q[k];
+      }
     }
     if (!first) continue;
-    const float x = j < K ? zj[j] : zt;
+    const float x = (j < K ? zj[j] : zt) - m;
     float v = 0.f;
-    if (hard) v += a1 * (i == tgt ? expm1f((x - m) - l1) : expf((x - m) - l1));
-    if (soft) v += at * (expf((x - m) * it - lt) - qs);
+    if (hard) v += a1 * (i == tgt ? expm1f(x - l1) : expf(x - l1));
+    if (soft) v += at * (expf(x * it - lt) - qs);
     d[i] = __float2bfloat16_rn(v);
   }
 }
@@ -233,134 +463,316 @@ __global__ void __launch_bounds__(KD_THREADS) distill_k(const bf16* logits, cons
 //   balance = alpha E / G sum_g sum_e f_e P_e, P_e = mean over valid t of p_te = softmax(logits_t)_e,
 //   z loss  = zc / G sum_g mean over valid t of lse_t^2,
 //   dlogit_te = alpha E / (G n) p_te (f_e - sum_j f_j p_tj) + 2 zc / (G n) lse_t p_te.
-constexpr int BAL_THREADS = 256;
+// f needs every choice of the group before the first gradient, but only the
+// choices (4 k bytes a token): a first kernel counts them, a second reads the
+// logits once and does everything else.  The second starts while the first
+// runs (programmatic launch) and waits for the counts only after its first
+// rows are loaded and their softmax is taken.
 constexpr int BAL_MAX_E = 512;
+constexpr int BAL_COUNT_THREADS = 512;
+constexpr int BAL_THREADS = 512;
 
-// Choices per expert and valid tokens of one group per block.
-__global__ void __launch_bounds__(BAL_THREADS) balance_count_k(const int32_t* __restrict__ idx,
-                                                               const uint8_t* __restrict__ valid, int S, int E, int k,
-                                                               int32_t* __restrict__ counts, int32_t* __restrict__ n) {
-  __shared__ int c[BAL_MAX_E + 1];
-  const int64_t g = blockIdx.x;
-  for (int e = threadIdx.x; e <= E; e += BAL_THREADS) c[e] = 0;
-  __syncthreads();
-  for (int64_t i = threadIdx.x; i < (int64_t)S * k; i += BAL_THREADS) {
-    const int64_t t = g * S + i / k;
-    if (valid && !valid[t]) continue;
-    if (i % k == 0) atomicAdd(&c[E], 1);
-    const int e = idx[g * S * k + i];
-    if (e >= 0 && e < E) atomicAdd(&c[e], 1);
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += BAL_THREADS) counts[g * E + e] = c[e];
-  if (threadIdx.x == 0) n[g] = c[E];
-}
-
-// Rows [b rows, (b + 1) rows) of a group per block: the rows' gradient, one warp
-// per row, and the block's sums of p and lse^2 (partial: [G][blocks][E + 1]).
-__global__ void __launch_bounds__(BAL_THREADS) balance_grad_k(const float* __restrict__ logits,
-                                                              const uint8_t* __restrict__ valid, int S, int E, int k,
-                                                              int rows, float alpha_g, float zc_g,
-                                                              const int32_t* __restrict__ counts,
-                                                              const int32_t* __restrict__ n, bf16* __restrict__ dlogits,
-                                                              float* __restrict__ partial) {
-  __shared__ float f[BAL_MAX_E];
-  __shared__ float acc[BAL_THREADS / 32][BAL_MAX_E + 1];
-  const int64_t g = blockIdx.y;
+// Choices per expert and valid tokens of one part of a group per block:
+// parts[g][part][e], the valid tokens at e = E.  A thread takes whole tokens,
+// four at a time so that their loads overlap.  The counters are laid out
+// [expert][lane], so that the lanes of a warp never meet in one bank or one
+// address; integer sums do not depend on the order of the atomics.
+__global__ void __launch_bounds__(BAL_COUNT_THREADS) balance_count_k(const int32_t* __restrict__ idx,
+                                                                     const uint8_t* __restrict__ valid, int S, int E,
+                                                                     int k, int per, int ldp,
+                                                                     int32_t* __restrict__ parts,
+                                                                     int* __restrict__ ticket) {
+  extern __shared__ int hist[];  // [E][32]
+  __shared__ int wn[BAL_COUNT_THREADS / 32];
+  dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float inv_n = n[g] > 0 ? 1.f / (float)n[g] : 0.f;
-  for (int e = threadIdx.x; e < E; e += BAL_THREADS) f[e] = (float)counts[g * E + e] * inv_n / (float)k;
-  for (int e = lane; e <= E; e += 32) acc[warp][e] = 0.f;
+  const int64_t g = blockIdx.y;
+  for (int i = threadIdx.x; i < E * 32; i += BAL_COUNT_THREADS) hist[i] = 0;
   __syncthreads();
-  const float cb = alpha_g * (float)E * inv_n, cz = 2.f * zc_g * inv_n;
-  const int r1 = min(S, (int)(blockIdx.x + 1) * rows);
-  for (int r = blockIdx.x * rows + warp; r < r1; r += BAL_THREADS / 32) {
-    const int64_t t = g * S + r;
-    const float* z = logits + t * E;
-    bf16* d = dlogits ? dlogits + t * E : nullptr;
-    if (valid && !valid[t]) {
-      if (d)
-        for (int e = lane; e < E; e += 32) d[e] = __float2bfloat16_rn(0.f);
-      continue;
+  int live = 0;
+  auto add = [&](int e) {
+    if (e >= 0 && e < E) atomicAdd(&hist[e * 32 + lane], 1);
+  };
+  const int t1 = min(S, (int)(blockIdx.x + 1) * per);
+  for (int t0 = (int)blockIdx.x * per + threadIdx.x; t0 < t1; t0 += 4 * BAL_COUNT_THREADS) {
+    bool on[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int t = t0 + u * BAL_COUNT_THREADS;
+      on[u] = t < t1 && (!valid || valid[g * S + t]);
+      live += on[u];
     }
-    float v[BAL_MAX_E / 32], m = -INFINITY, s = 0.f, mean = 0.f;
+    for (int i = 0; i < k; i += 4) {
+      int4 q[4];
 #pragma unroll
-    for (int j = 0; j < BAL_MAX_E / 32; ++j) {
-      v[j] = j * 32 + lane < E ? z[j * 32 + lane] : -INFINITY;
-      m = fmaxf(m, v[j]);
-    }
-    m = warp_max(m);
-#pragma unroll
-    for (int j = 0; j < BAL_MAX_E / 32; ++j)
-      if (j * 32 + lane < E) {
-        v[j] = expf(v[j] - m);
-        s += v[j];
+      for (int u = 0; u < 4; ++u) {
+        const int32_t* p = idx + (g * S + t0 + u * BAL_COUNT_THREADS) * k + i;
+        q[u] = make_int4(-1, -1, -1, -1);
+        if (!on[u]) continue;
+        if ((k & 3) == 0) {
+          q[u] = *reinterpret_cast<const int4*>(p);
+        } else {
+          q[u].x = p[0];
+          if (i + 1 < k) q[u].y = p[1];
+          if (i + 2 < k) q[u].z = p[2];
+          if (i + 3 < k) q[u].w = p[3];
+        }
       }
-    s = warp_sum(s);
-    const float lse = m + logf(s), is = 1.f / s;
 #pragma unroll
-    for (int j = 0; j < BAL_MAX_E / 32; ++j)
-      if (j * 32 + lane < E) {
-        v[j] *= is;
-        mean += f[j * 32 + lane] * v[j];
-        acc[warp][j * 32 + lane] += v[j];
+      for (int u = 0; u < 4; ++u) {
+        add(q[u].x);
+        add(q[u].y);
+        add(q[u].z);
+        add(q[u].w);
       }
-    mean = warp_sum(mean);
-    if (lane == 0) acc[warp][E] += lse * lse;
-    if (d) {
-#pragma unroll
-      for (int j = 0; j < BAL_MAX_E / 32; ++j)
-        if (j * 32 + lane < E)
-          d[j * 32 + lane] = __float2bfloat16_rn(v[j] * (cb * (f[j * 32 + lane] - mean) + cz * lse));
     }
   }
+  live = __reduce_add_sync(0xffffffffu, live);
+  if (lane == 0) wn[warp] = live;
   __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += BAL_THREADS) {
-    float a = 0.f;
+  int32_t* out = parts + (g * gridDim.x + blockIdx.x) * ldp;
+  for (int e = warp; e < E; e += BAL_COUNT_THREADS / 32) {
+    const int c = __reduce_add_sync(0xffffffffu, hist[e * 32 + lane]);
+    if (lane == 0) out[e] = c;
+  }
+  if (threadIdx.x == 0) {
+    int c = 0;
 #pragma unroll
-    for (int w = 0; w < BAL_THREADS / 32; ++w) a += acc[w][e];
-    partial[(g * gridDim.x + blockIdx.x) * (E + 1) + e] = a;
+    for (int w = 0; w < BAL_COUNT_THREADS / 32; ++w) c += wn[w];
+    out[E] = c;
+    if (blockIdx.x == 0) {
+      ticket[1 + g] = 0;
+      if (g == 0) ticket[0] = 0;
+    }
   }
 }
 
-// Group sums of the blocks' partials in block order: prob, and the group's two losses.
-__global__ void __launch_bounds__(BAL_THREADS) balance_group_k(const float* __restrict__ partial, int nblk, int E, int k,
-                                                               const int32_t* __restrict__ counts,
-                                                               const int32_t* __restrict__ n, float* __restrict__ prob,
-                                                               float2* __restrict__ gloss) {
-  __shared__ float red[BAL_THREADS / 32];
-  const int64_t g = blockIdx.x;
-  const float inv_n = n[g] > 0 ? 1.f / (float)n[g] : 0.f;
-  float lb = 0.f, lz = 0.f;
-  for (int e = threadIdx.x; e <= E; e += BAL_THREADS) {
-    float a = 0.f;
-    for (int b = 0; b < nblk; ++b) a += partial[(g * nblk + b) * (E + 1) + e];
-    a *= inv_n;
-    if (e < E) {
-      prob[g * E + e] = a;
-      lb += (float)counts[g * E + e] * inv_n / (float)k * a;
+struct BalArgs {
+  const float* logits;
+  const uint8_t* valid;
+  int64_t G;
+  int S, E, k, rows, nblk, ldp;
+  float alpha, z_coef;  // both over G
+  int nparts;
+  const int32_t* parts;  // [G][nparts][ldp] of the counting kernel
+  int32_t* counts;
+  bf16* dlogits;
+  float *prob, *loss;
+  float* partial;  // [G][nblk][ldp]: E sums of p, the sum of lse^2, zeros
+  float2* gloss;   // [G]
+  int* ticket;     // [1 + G], zeroed by the counting kernel
+};
+
+// LPR lanes share a row, each holding NV vectors of 8 logits (vector j of a
+// lane: elements 8 (j LPR + lane) ..); VEC: E is a multiple of 8 and rows are
+// read and written as 16-byte vectors.  A block takes a.rows rows of one group;
+// the block that finishes a group last adds the blocks' sums in block order,
+// and the one that finishes the last group adds the groups' losses.
+template <int LPR, int NV, bool VEC>
+__global__ void __launch_bounds__(BAL_THREADS, NV == 1 ? 2 : 1) balance_grad_k(const BalArgs a) {
+  constexpr int RPB = BAL_THREADS / LPR;  // rows in flight per block
+  constexpr int WARPS = BAL_THREADS / 32;
+  constexpr int NE = LPR * NV * 8;        // columns the lanes of a row cover
+  __shared__ float acc[WARPS][NE + 1];
+  __shared__ __align__(16) float tree[4 * BAL_THREADS];
+  __shared__ float red[WARPS];
+  __shared__ int last;
+  __shared__ int cnt[NE + 1];  // the group's choices per expert, its valid tokens at E
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int sub = tid % LPR, slot = tid / LPR;
+  const int64_t g = blockIdx.y;
+  const int E = a.E;
+  const int r1 = min(a.S, (int)(blockIdx.x + 1) * a.rows);
+  float x[NV * 8], f[NV * 8], P[NV * 8], zz = 0.f;
+  bool on;
+  auto load = [&](int r) {
+    const int64_t t = g * a.S + r;
+    on = r < r1 && (!a.valid || a.valid[t]);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int e = (j * LPR + sub) * 8;
+      if (VEC) {
+        float4 u = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY), w = u;
+        if (on && e < E) {
+          u = *reinterpret_cast<const float4*>(a.logits + t * E + e);
+          w = *reinterpret_cast<const float4*>(a.logits + t * E + e + 4);
+        }
+        x[8 * j] = u.x; x[8 * j + 1] = u.y; x[8 * j + 2] = u.z; x[8 * j + 3] = u.w;
+        x[8 * j + 4] = w.x; x[8 * j + 5] = w.y; x[8 * j + 6] = w.z; x[8 * j + 7] = w.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[8 * j + i] = on && e + i < E ? a.logits[t * E + e + i] : -INFINITY;
+      }
+    }
+  };
+  auto over_row = [&](float v, auto op) {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  };
+  auto sum = [](float u, float w) { return u + w; };
+  auto mx = [](float u, float w) { return fmaxf(u, w); };
+#pragma unroll
+  for (int i = 0; i < NV * 8; ++i) P[i] = f[i] = 0.f;
+  int r = (int)blockIdx.x * a.rows + slot;
+  load(r);
+  float cb = 0.f, cz = 0.f, inv_n = 0.f;
+  bool started = false;
+  // the same number of turns for every lane of a warp: the shuffles are warp-wide
+  for (int base = (int)blockIdx.x * a.rows; base < r1; base += RPB, r += RPB) {
+    const bool now = on;
+    float m = -INFINITY, s = 0.f, fe = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV * 8; ++i) m = fmaxf(m, x[i]);
+    m = over_row(m, mx);
+    float e8[NV * 8];
+#pragma unroll
+    for (int i = 0; i < NV * 8; ++i) {
+      e8[i] = x[i] == -INFINITY && m != -INFINITY ? 0.f : expf(x[i] - m);
+      s += e8[i];
+    }
+    const bool pad_lanes = !now;  // rows outside the block or padded: nothing below counts
+    load(r + RPB);                // the next row is on its way while this one is worked on
+    if (!started) {
+      started = true;
+      dep_wait();  // the counts and the tickets
+      for (int i = tid; i <= E; i += BAL_THREADS) cnt[i] = 0;
+      __syncthreads();
+      const int32_t* pc = a.parts + g * a.nparts * a.ldp;
+      const int lanes = max(1, BAL_THREADS / (E + 1));  // threads that share a column, each taking every lanes-th part
+      for (int i = tid; i < lanes * (E + 1); i += BAL_THREADS) {
+        const int e = i % (E + 1);
+        int c = 0;
+#pragma unroll 8
+        for (int q = i / (E + 1); q < a.nparts; q += lanes) c += pc[q * a.ldp + e];
+        atomicAdd(&cnt[e], c);
+      }
+      __syncthreads();
+      const int n = cnt[E];
+      if (blockIdx.x == 0)
+        for (int e = tid; e < E; e += BAL_THREADS) a.counts[g * E + e] = cnt[e];
+      inv_n = n > 0 ? 1.f / (float)n : 0.f;
+      cb = a.alpha * (float)E * inv_n;
+      cz = 2.f * a.z_coef * inv_n;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int e = (j * LPR + sub) * 8 + i;
+          if (e < E) f[8 * j + i] = (float)cnt[e] * inv_n / (float)a.k;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV * 8; ++i) fe += f[i] * e8[i];
+    s = over_row(s, sum);
+    fe = over_row(fe, sum);
+    const float is = 1.f / s, lse = m + logf(s), mean = fe * is, shift = cz * lse - cb * mean;
+    if (!pad_lanes) {
+#pragma unroll
+      for (int i = 0; i < NV * 8; ++i) {
+        const int e = ((i >> 3) * LPR + sub) * 8 + (i & 7);
+        const float p = e < E ? e8[i] * is : 0.f;
+        P[i] += p;
+        e8[i] = p * (cb * f[i] + shift);
+      }
+      if (sub == 0) zz += lse * lse;
     } else {
-      lz = a;
+#pragma unroll
+      for (int i = 0; i < NV * 8; ++i) e8[i] = 0.f;
+    }
+    if (a.dlogits && r < r1) {
+      bf16* d = a.dlogits + (g * a.S + r) * E;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int e = (j * LPR + sub) * 8;
+        if (VEC) {
+          if (e < E) {
+            float o8[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o8[i] = e8[8 * j + i];
+            *reinterpret_cast<uint4*>(d + e) = pack8(o8);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (e + i < E) d[e + i] = __float2bfloat16_rn(e8[8 * j + i]);
+        }
+      }
+    }
+  }
+  // the block's sums: rows of a warp by shuffles, warps in warp order
+#pragma unroll
+  for (int i = 0; i < NV * 8; ++i) {
+#pragma unroll
+    for (int o = 16; o >= LPR; o >>= 1) P[i] += __shfl_xor_sync(0xffffffffu, P[i], o);
+    if (lane < LPR) acc[warp][((i >> 3) * LPR + sub) * 8 + (i & 7)] = P[i];
+  }
+  zz = warp_sum(zz);
+  if (lane == 0) acc[warp][NE] = zz;
+  __syncthreads();
+  float* part = a.partial + (g * a.nblk + blockIdx.x) * a.ldp;
+  for (int e = tid; e < a.ldp; e += BAL_THREADS) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) v += e <= E ? acc[w][e < E ? e : NE] : 0.f;
+    part[e] = v;
+  }
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) last = atomicAdd(&a.ticket[1 + g], 1) == a.nblk - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  // the group: thread (c, q) adds the four columns q of blocks c, c + C, ... in order, then the C parts in order
+  const int c4 = a.ldp / 4, C = max(1, min(a.nblk, BAL_THREADS / c4));
+  const float4* all = reinterpret_cast<const float4*>(a.partial + g * a.nblk * a.ldp);
+  if (tid < C * c4) {
+    const int c = tid / c4, q = tid % c4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int b = c; b < a.nblk; b += C) {
+      const float4 u = __ldcg(all + (int64_t)b * c4 + q);
+      v.x += u.x;
+      v.y += u.y;
+      v.z += u.z;
+      v.w += u.w;
+    }
+    reinterpret_cast<float4*>(tree)[tid] = v;
+  }
+  __syncthreads();
+  float lb = 0.f, lz = 0.f;
+  for (int e = tid; e <= E; e += BAL_THREADS) {
+    float v = 0.f;
+    for (int c = 0; c < C; ++c) v += tree[c * a.ldp + e];
+    v *= inv_n;
+    if (e < E) {
+      a.prob[g * E + e] = v;
+      lb += (float)cnt[e] * inv_n / (float)a.k * v;
+    } else {
+      lz = v;
     }
   }
   lb = block_sum<BAL_THREADS>(lb, red);
   lz = block_sum<BAL_THREADS>(lz, red);
-  if (threadIdx.x == 0) gloss[g] = make_float2(lb, lz);
-}
-
-__global__ void __launch_bounds__(BAL_THREADS) balance_loss_k(const float2* __restrict__ gloss, int64_t G,
-                                                              float scale_b, float scale_z, float* __restrict__ loss) {
-  __shared__ float red[BAL_THREADS / 32];
-  float b = 0.f, z = 0.f;
-  for (int64_t g = threadIdx.x; g < G; g += BAL_THREADS) {
-    b += gloss[g].x;
-    z += gloss[g].y;
+  if (tid == 0) {
+    a.gloss[g] = make_float2(lb, lz);
+    __threadfence();
+    last = atomicAdd(&a.ticket[0], 1) == a.G - 1;
   }
-  b = block_sum<BAL_THREADS>(b, red);
-  z = block_sum<BAL_THREADS>(z, red);
-  if (threadIdx.x == 0) {
-    loss[0] = b * scale_b;
-    loss[1] = z * scale_z;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  lb = lz = 0.f;
+  for (int64_t i = tid; i < a.G; i += BAL_THREADS) {
+    const float2 v = __ldcg(a.gloss + i);
+    lb += v.x;
+    lz += v.y;
+  }
+  lb = block_sum<BAL_THREADS>(lb, red);
+  lz = block_sum<BAL_THREADS>(lz, red);
+  if (tid == 0) {
+    a.loss[0] = lb * a.alpha * (float)E;
+    a.loss[1] = lz * a.z_coef;
   }
 }
 
@@ -371,25 +783,47 @@ inline int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 // many as fit kPieceBytes, at least 1024 (a chunk re-reads the weights for
 // every product, so short chunks are bound by memory), the chunks of one call
 // equal up to the 256-row tile.
-constexpr int64_t kPieceBytes = (int64_t)1 << 30;
+constexpr int64_t kBalBlocks = 304;  // two blocks of 512 threads on each SM
+constexpr int64_t kPieceBytes = (int64_t)3 << 30;
 int64_t ce_chunk(int64_t T, int V) {
   int64_t most = kPieceBytes / (2 * up(V, 64)) / 256 * 256;
-  if (most < 1024) most = 1024;
+  if (most < 2048) most = 2048;
   if (T <= most) return T;
   const int64_t n = (T + most - 1) / most;
   return up((T + n - 1) / n, 256);
+}
+
+// Runs that the sum over V of a chunk's dh is cut into.  Its tiles are long (V
+// / 64 K blocks each) and few (rows / 256 by H / 256); they go first and dW's
+// short tiles fill up behind them, so a cut is needed only where the last long
+// tile would end after its share of all work: 76 CTA pairs, a K block as the
+// unit, 10 of them for an epilogue that no main loop hides (few rows).  A cut
+// has to save 24 units (about 8 us), what adding the runs costs.
+int ce_runs(int64_t rows, int H, int V, bool dW) {
+  const int64_t pairs = 76, nh = (H + 255) / 256, n = (rows + 255) / 256 * nh, nk = (V + 63) / 64;
+  if (n >= 2 * pairs) return 1;  // two waves and more even out
+  const int64_t w = (rows + 63) / 64 < 10 ? 10 : (rows + 63) / 64;
+  const double share = ((double)n * nk + (dW ? (double)((V + 255) / 256) * nh * w : 0.0)) / pairs;
+  auto end = [&](int64_t k) { return (double)((n * k + pairs - 1) / pairs * ((nk + k - 1) / k)); };
+  int best = 1;
+  for (int k = 2; k <= 32 && nk / k >= 8 && end(best) > 1.05 * share; ++k) {
+    const int64_t per = (nk + k - 1) / k;
+    if ((nk + per - 1) / per != k) continue;  // the last run would be empty
+    if (end(k) < end(best) - (best == 1 ? 24.0 : 0.0)) best = k;
+  }
+  return best;
 }
 
 struct CeScratch {
   int* ctr;
   float2* stat;
   float* zt;
-  bf16* E;
-  float* dWacc;
+  uint16_t* E;
+  float *dWacc, *slabs;
   int64_t ldE, chunk;
-  int npieces;
+  int npieces, runs;
 };
-size_t ce_carve(int64_t T, int H, int V, bool grads, uint8_t* base, CeScratch* w) {
+size_t ce_carve(int64_t T, int H, int V, bool grads, bool dW, uint8_t* base, CeScratch* w) {
   size_t off = 0;
   auto take = [&](int64_t bytes) {
     uint8_t* p = base ? base + off : nullptr;
@@ -402,8 +836,13 @@ size_t ce_carve(int64_t T, int H, int V, bool grads, uint8_t* base, CeScratch* w
   w->ctr = (int*)take(256);
   w->stat = (float2*)take(w->chunk * w->npieces * 8);
   w->zt = (float*)take(w->chunk * 4);
-  w->E = grads ? (bf16*)take(w->chunk * w->ldE * 2) : nullptr;
+  w->E = grads ? (uint16_t*)take(w->chunk * w->ldE * 2) : nullptr;
   w->dWacc = grads && w->chunk < T ? (float*)take((int64_t)V * H * 4) : nullptr;
+  // the runs with dW beside them or without: room for the larger number
+  const int a = grads ? ce_runs(w->chunk, H, V, true) : 1, b = grads ? ce_runs(w->chunk, H, V, false) : 1;
+  w->runs = dW ? a : b;
+  const int most = a > b ? a : b;
+  w->slabs = most > 1 ? (float*)take((int64_t)most * w->chunk * H * 4) : nullptr;
   return off;
 }
 bool ce_shape_ok(int64_t T, int H, int V) {
@@ -411,10 +850,11 @@ bool ce_shape_ok(int64_t T, int H, int V) {
 }
 
 struct BalScratch {
-  int32_t* n;
+  int32_t* parts;
+  int* ticket;
   float2* gloss;
   float* partial;
-  int nblk, rows;
+  int nblk, rows, ldp, nparts;
 };
 size_t bal_carve(int64_t T, int S, int E, uint8_t* base, BalScratch* w) {
   size_t off = 0;
@@ -424,18 +864,64 @@ size_t bal_carve(int64_t T, int S, int E, uint8_t* base, BalScratch* w) {
     return p;
   };
   const int64_t G = T / S;
-  int64_t blk = (608 + G - 1) / G;  // about four blocks per SM in all
-  const int64_t most = (S + 7) / 8;
+  int64_t blk = (kBalBlocks + G - 1) / G;
+  const int64_t most = (S + 31) / 32;  // a block has at least 32 rows to take
   if (blk > most) blk = most;
   w->rows = (int)((S + blk - 1) / blk);
   w->nblk = (S + w->rows - 1) / w->rows;
-  w->n = (int32_t*)take(G * 4);
+  // counting blocks of a group: at least 512 tokens each, 64 at most in all
+  const int64_t parts = (S + 511) / 512, cap = (64 + G - 1) / G;
+  w->nparts = (int)(parts < cap ? parts : cap);
+  w->ldp = (int)up(E + 1, 4);
+  w->parts = (int32_t*)take(G * w->nparts * w->ldp * 4);
+  w->ticket = (int*)take((1 + G) * 4);
   w->gloss = (float2*)take(G * 8);
-  w->partial = (float*)take(G * w->nblk * (E + 1) * 4);
+  w->partial = (float*)take(G * w->nblk * w->ldp * 4);
   return off;
 }
 bool bal_shape_ok(int64_t T, int S, int E) {
   return T >= 0 && S > 0 && T % S == 0 && T / S <= 65535 && E >= 1 && E <= BAL_MAX_E;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, bool dependent,
+                   cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (cluster > 0) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = (unsigned)cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (dependent) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int LPR, int NV>
+cudaError_t launch_balance_grad(const BalArgs& a, cudaStream_t s) {
+  const dim3 grid((unsigned)a.nblk, (unsigned)a.G);
+  return a.E % 8 == 0 ? launch(balance_grad_k<LPR, NV, true>, grid, BAL_THREADS, 0, 0, true, s, a)
+                      : launch(balance_grad_k<LPR, NV, false>, grid, BAL_THREADS, 0, 0, true, s, a);
+}
+
+template <int NV, int NT = 256>
+cudaError_t launch_distill(const KdArgs& a, int64_t rows, int cluster, cudaStream_t s) {
+  return launch(distill_k<NV, NT>, dim3((unsigned)(rows * cluster)), NT, (size_t)((a.K + 3) & ~3) * 16, cluster, false,
+                s, a);
 }
 
 }  // namespace
@@ -444,7 +930,7 @@ bool bal_shape_ok(int64_t T, int S, int E) {
 size_t linear_cross_entropy_scratch(int64_t T, int H, int V, bool grads) {
   if (!ce_shape_ok(T, H, V)) return 0;
   CeScratch w;
-  return ce_carve(T, H, V, grads, nullptr, &w);
+  return ce_carve(T, H, V, grads, true, nullptr, &w);
 }
 
 cudaError_t linear_cross_entropy(const bf16* h, const bf16* W, const int32_t* target, int64_t T, int H, int V, float g,
@@ -455,7 +941,7 @@ cudaError_t linear_cross_entropy(const bf16* h, const bf16* W, const int32_t* ta
       (reinterpret_cast<uintptr_t>(scratch) & 255))
     return cudaErrorInvalidValue;
   CeScratch w;
-  if (ce_carve(T, H, V, grads, (uint8_t*)scratch, &w) > scratch_bytes) return cudaErrorInvalidValue;
+  if (ce_carve(T, H, V, grads, dW != nullptr, (uint8_t*)scratch, &w) > scratch_bytes) return cudaErrorInvalidValue;
   if (T == 0) return cudaSuccess;
   cudaError_t e = cudaMemsetAsync(w.ctr, 0, 256, s);
   if (e != cudaSuccess) return e;
@@ -465,19 +951,27 @@ cudaError_t linear_cross_entropy(const bf16* h, const bf16* W, const int32_t* ta
     const SoftmaxPieces sp{w.stat, w.npieces, target + c0, w.zt, w.E, w.ldE};
     e = gemm_softmax_pieces(h + c0 * H, W, rows, V, H, sp, w.ctr, s);
     if (e != cudaSuccess) return e;
-    ce_join_k<<<rows, JOIN_THREADS, w.npieces * sizeof(float), s>>>(w.stat, w.npieces, target + c0, w.zt, V, g,
-                                                                    row_loss + c0, w.E, w.ldE);
+    // few rows: several blocks share each, down to about 2048 columns a block
+    const int want = 1216 / rows, most = (V + 2047) / 2048, split = want < 1 || !w.E ? 1 : want < most ? want : most;
+    ce_join_k<<<dim3((unsigned)rows, (unsigned)split), JOIN_THREADS, 0, s>>>(w.stat, w.npieces, target + c0, w.zt, V,
+                                                                             row_loss + c0, w.E, w.ldE);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (!grads) continue;
-    GemmArgs gd{w.E, w.ldE, 0, W, H, 1, rows, H, V, dh ? dh + c0 * H : nullptr, H, nullptr, 0, nullptr, 0, 0};
-    GemmArgs gw{w.E, w.ldE, 1, h + c0 * H, H, 1, V, H, rows, last ? dW : nullptr, H, nullptr, 0, nullptr, H, 0};
+    const bf16* d = reinterpret_cast<const bf16*>(w.E);
+    const GemmArgs gd{d, w.ldE, 0, W, H, 1, rows, H, V, dh ? dh + c0 * H : nullptr, H, nullptr, 0, nullptr, 0, 0};
+    GemmArgs gw{d, w.ldE, 1, h + c0 * H, H, 1, V, H, rows, last ? dW : nullptr, H, nullptr, 0, nullptr, H, 0};
     if (w.dWacc) {
       gw.Dacc = w.dWacc;
       gw.acc_mode = first ? 1 : 2;
     }
-    if (dh && dW) e = gemm_grads(gd, gw, w.ctr, s);
-    else e = gemm_one(dh ? gd : gw, w.ctr, s);
+    e = gemm_grads(GradArgs{dh ? &gd : nullptr, dW ? &gw : nullptr, g, w.runs, w.slabs, w.ctr}, s);
     if (e != cudaSuccess) return e;
+    if (dh && w.runs > 1) {
+      const int64_t n4 = (int64_t)rows * H / 4;
+      ce_add_runs_k<<<(unsigned)((n4 + 255) / 256), 256, 0, s>>>(reinterpret_cast<const float4*>(w.slabs), n4, w.runs, g,
+                                                                reinterpret_cast<uint2*>(dh + c0 * H));
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
   }
   return cudaSuccess;
 }
@@ -488,10 +982,32 @@ cudaError_t distill_topk(const bf16* logits, const int32_t* target, const float*
   if (rows < 0 || rows > 0x7fffffff || V < 1 || K < 1 || K > KD_MAX_K || !(tau > 0.f) || !(tau < INFINITY) || !(1.f / tau < INFINITY) || !al16(logits) ||
       !al16(dlogits))
     return cudaErrorInvalidValue;
+  // vectors a row touches at most: rows of an odd V start anywhere in one
+  const int nvec = V % 8 == 0 ? V / 8 : (V + 14) / 8;
+  if (V > KD_MAX_V || nvec > KD_MAX_V / 8) return cudaErrorInvalidValue;
   if (rows == 0) return cudaSuccess;
-  distill_k<<<(unsigned)rows, KD_THREADS, 0, s>>>(logits, target, t_val, t_idx, V, K, tau, w_ce, w_kd, row_ce, row_kd,
-                                                  dlogits);
-  return cudaGetLastError();
+  const KdArgs a{logits, target, t_val, t_idx, V, K, tau, w_ce, w_kd, row_ce, row_kd, dlogits};
+  // blocks of a cluster so that a thread holds up to 9 vectors (more at the
+  // widest rows, where the cluster is at its largest)
+  int cluster = 1;
+  while (cluster < KD_MAX_CLUSTER && (nvec + cluster - 1) / cluster > 9 * 224) cluster *= 2;
+  if (rows * cluster > 0x7fffffff) return cudaErrorInvalidValue;
+  const int per = (nvec + cluster - 1) / cluster;
+  switch ((per + 223) / 224) {
+    case 1: return launch_distill<1>(a, rows, cluster, s);
+    case 2: return launch_distill<2>(a, rows, cluster, s);
+    case 3: return launch_distill<3>(a, rows, cluster, s);
+    case 4: return launch_distill<4>(a, rows, cluster, s);
+    case 5: return launch_distill<5>(a, rows, cluster, s);
+    case 6: return launch_distill<6>(a, rows, cluster, s);
+    case 7: return launch_distill<7>(a, rows, cluster, s);
+    case 8: return launch_distill<8>(a, rows, cluster, s);
+    case 9: return launch_distill<9>(a, rows, cluster, s);
+    case 10: case 11: return launch_distill<11>(a, rows, cluster, s);
+    case 12: case 13: return launch_distill<13>(a, rows, cluster, s);
+    case 14: case 15: return launch_distill<15>(a, rows, cluster, s);
+    default: return launch_distill<KD_WIDE_NV, 512>(a, rows, cluster, s);
+  }
 }
 
 size_t router_balance_scratch(int64_t T, int S, int E) {
@@ -503,20 +1019,31 @@ size_t router_balance_scratch(int64_t T, int S, int E) {
 cudaError_t router_balance(const float* logits, const int32_t* idx, const uint8_t* valid, int64_t T, int S, int E,
                            int k, float alpha, float z_coef, float* loss, int32_t* counts, float* prob, bf16* dlogits,
                            void* scratch, size_t scratch_bytes, cudaStream_t s) {
-  if (!bal_shape_ok(T, S, E) || k < 1 || k > E || (int64_t)S * k > 0x7fffffff || !al16(logits) || !al16(dlogits) ||
+  if (!bal_shape_ok(T, S, E) || k < 1 || k > E || (int64_t)S * k > 0x7fffffff || !al16(logits) || !al16(dlogits) || !al16(idx) ||
       (reinterpret_cast<uintptr_t>(scratch) & 255))
     return cudaErrorInvalidValue;
   if (T == 0) return cudaSuccess;
   BalScratch w;
   if (bal_carve(T, S, E, (uint8_t*)scratch, &w) > scratch_bytes) return cudaErrorInvalidValue;
   const int64_t G = T / S;
-  const float per_group = 1.f / (float)G;
-  balance_count_k<<<(unsigned)G, BAL_THREADS, 0, s>>>(idx, valid, S, E, k, counts, w.n);
-  balance_grad_k<<<dim3((unsigned)w.nblk, (unsigned)G), BAL_THREADS, 0, s>>>(
-      logits, valid, S, E, k, w.rows, alpha * per_group, z_coef * per_group, counts, w.n, dlogits, w.partial);
-  balance_group_k<<<(unsigned)G, BAL_THREADS, 0, s>>>(w.partial, w.nblk, E, k, counts, w.n, prob, w.gloss);
-  balance_loss_k<<<1, BAL_THREADS, 0, s>>>(w.gloss, G, alpha * per_group * (float)E, z_coef * per_group, loss);
-  return cudaGetLastError();
+  const size_t smem = (size_t)E * 32 * sizeof(int);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024)  // per device, so set on every call that needs it
+    e = cudaFuncSetAttribute(balance_count_k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int per = (S + w.nparts - 1) / w.nparts;
+  balance_count_k<<<dim3((unsigned)w.nparts, (unsigned)G), BAL_COUNT_THREADS, smem, s>>>(idx, valid, S, E, k, per, w.ldp,
+                                                                                        w.parts, w.ticket);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const BalArgs a{logits, valid, G, S, E, k, w.rows, w.nblk, w.ldp, alpha / (float)G, z_coef / (float)G, w.nparts,
+                  w.parts, counts, dlogits, prob, loss, w.partial, w.gloss, w.ticket};
+  if (E <= 8) return launch_balance_grad<1, 1>(a, s);
+  if (E <= 16) return launch_balance_grad<2, 1>(a, s);
+  if (E <= 32) return launch_balance_grad<4, 1>(a, s);
+  if (E <= 64) return launch_balance_grad<8, 1>(a, s);
+  if (E <= 128) return launch_balance_grad<16, 1>(a, s);
+  if (E <= 256) return launch_balance_grad<32, 1>(a, s);
+  return launch_balance_grad<32, 2>(a, s);
 }
 
 }  // namespace mt

@@ -63,26 +63,34 @@ cudaError_t gemm_expert_kgroups(const GemmKGroupArgs& g, cudaStream_t s);
 // Softmax statistics of logits Z = A B^T ([M][N], K-major operands with row
 // stride K) that are never written: per row and piece of 256 columns, (m, s) =
 // (largest logit, sum exp(z - m) without the target's column) from the FP32
-// accumulators; with E, also E[m, n] = bf16_rne(exp(z - m of its piece)), 0 at
-// the target; zt[r] = the logit of column target[r] (rows whose target is
-// outside [0, N) leave zt as it was).  K a
-// multiple of 8, A, B and E 16-byte aligned, ldE a multiple of 8.
+// accumulators; with E, also E[m, n] = fp16_rne(2^15 exp(z - m of its piece)),
+// 0 at the target; zt[r] = the logit of column target[r] (rows whose target is
+// outside [0, N) leave zt as it was).  K a multiple of 8, A, B and E 16-byte
+// aligned, ldE a multiple of 8.
 struct SoftmaxPieces {
   float2* stat;           // [M][npieces]
   int npieces;            // ceil(N / 256)
   const int32_t* target;  // [M]
   float* zt;              // [M]
-  bf16* E; int64_t ldE;   // null: statistics only
+  uint16_t* E; int64_t ldE;  // null: statistics only
 };
 // tile_ctr: the launch's tile counter, zero on entry and left zero; the caller's
 // memory, so that launches of different callers share nothing.
 cudaError_t gemm_softmax_pieces(const bf16* A, const bf16* B, int M, int N, int K, const SoftmaxPieces& sp,
                                 int* tile_ctr, cudaStream_t s);
-// dX = dY W (a_mn = 0, b_mn = 1) and dW = dY^T X (a_mn = b_mn = 1) in one
-// launch with the caller's tile counter, the input gradient's tiles (the long
-// sums of an LM head) first; and either of them alone.
-cudaError_t gemm_grads(const GemmArgs& dgrad, const GemmArgs& wgrad, int* tile_ctr, cudaStream_t s);
-cudaError_t gemm_one(const GemmArgs& g, int* tile_ctr, cudaStream_t s);
+// alpha dY W (a_mn = 0, b_mn = 1) and alpha dY^T X (a_mn = b_mn = 1), one of
+// them or both in one launch, the input gradient's tiles (the long sums of an
+// LM head) first.  alpha applies to D, not to Dacc.  ksplit > 1: the input
+// gradient's sum is cut into ksplit equal runs of K blocks (none may be empty)
+// whose FP32 products go to slabs [ksplit][M][N]; the caller adds them.
+struct GradArgs {
+  const GemmArgs *dgrad, *wgrad;
+  float alpha;
+  int ksplit;
+  float* slabs;
+  int* tile_ctr;  // as above
+};
+cudaError_t gemm_grads(const GradArgs& g, cudaStream_t s);
 // Test hook: the next `launches` GEMM launches issue no loads, so their bounded
 // waits expire and they report through the kernel error word.
 void gemm_inject_stall(int launches);

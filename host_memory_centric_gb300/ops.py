@@ -140,26 +140,33 @@ def cross_entropy(logits, target, inv_norm, row_loss):
     _chk(_L().mt_cross_entropy(_p(logits), _p(target), rows, V, inv_norm, _p(row_loss), _stream()))
 
 
-def _want(name, t, dtype, shape, optional=False):
-    """Refuses a tensor the library would misread: another type, shape, stride or device."""
+def _refuse(msg):
     from . import MtError
-    if t is None:
-        if optional:
-            return
-        raise MtError(-1, f"{name} is missing")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise MtError(-1, f"{name}: want a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
-                          f"{tuple(t.shape)} with strides {t.stride()}")
+    raise MtError(-1, msg)
+
+
+def _device(name, t):
+    """The current CUDA device's index, which t (and every other argument) has
+    to be on: the launch goes to that device's current stream."""
     import torch
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise MtError(-1, f"{name} is on {t.device}, not on the current CUDA device")
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        _refuse(f"{name} is on {t.device}, not on the current CUDA device")
+    return dev
 
 
-def _want_scratch(scratch, nbytes):
-    from . import MtError
-    if scratch is None or not scratch.is_contiguous() or scratch.device.type != "cuda" \
-            or scratch.numel() * scratch.element_size() < nbytes:
-        raise MtError(-1, f"scratch: want {nbytes} bytes of contiguous device memory")
+def _want(name, t, dtype, shape, dev):
+    """Refuses a tensor the library would misread: another type, shape, stride or device."""
+    if t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}"
+        _refuse(f"{name}: want a contiguous {dtype} tensor of shape {shape} on CUDA device {dev}, got {got}")
+
+
+def _scratch(t, dev):
+    """Bytes of a workspace; the library itself refuses one that is too small."""
+    if t is None or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(f"scratch: want contiguous memory of CUDA device {dev}")
+    return t.numel() * t.element_size()
 
 
 def linear_cross_entropy_scratch_bytes(T, H, V, grads=True) -> int:
@@ -174,13 +181,15 @@ def linear_cross_entropy(h, W, target, inv_norm, row_loss, dh, dW, scratch):
     bf = torch.bfloat16
     T, H = h.shape
     V = W.shape[0]
-    _want("h", h, bf, (T, H)); _want("W", W, bf, (V, H)); _want("target", target, torch.int32, (T,))
-    _want("row_loss", row_loss, torch.float32, (T,))
-    _want("dh", dh, bf, (T, H), True); _want("dW", dW, bf, (V, H), True)
-    grads = dh is not None or dW is not None
-    _want_scratch(scratch, linear_cross_entropy_scratch_bytes(T, H, V, grads))
+    dev = _device("h", h)
+    _want("h", h, bf, (T, H), dev); _want("W", W, bf, (V, H), dev); _want("target", target, torch.int32, (T,), dev)
+    _want("row_loss", row_loss, torch.float32, (T,), dev)
+    if dh is not None:
+        _want("dh", dh, bf, (T, H), dev)
+    if dW is not None:
+        _want("dW", dW, bf, (V, H), dev)
     _chk(_L().mt_linear_cross_entropy(_p(h), _p(W), _p(target), T, H, V, inv_norm, _p(row_loss), _p(dh), _p(dW),
-                                      _p(scratch), scratch.numel() * scratch.element_size(), _stream()))
+                                      _p(scratch), _scratch(scratch, dev), _stream()))
 
 
 def distill_topk(logits, target, t_val, t_idx, tau, w_ce, w_kd, row_ce, row_kd, dlogits):
@@ -190,10 +199,15 @@ def distill_topk(logits, target, t_val, t_idx, tau, w_ce, w_kd, row_ce, row_kd, 
     import torch
     rows, V = logits.shape
     K = t_val.shape[1]
-    _want("logits", logits, torch.bfloat16, (rows, V)); _want("target", target, torch.int32, (rows,), True)
-    _want("t_val", t_val, torch.float32, (rows, K)); _want("t_idx", t_idx, torch.int32, (rows, K))
-    _want("row_ce", row_ce, torch.float32, (rows,), True); _want("row_kd", row_kd, torch.float32, (rows,))
-    _want("dlogits", dlogits, torch.bfloat16, (rows, V), True)
+    dev = _device("logits", logits)
+    _want("logits", logits, torch.bfloat16, (rows, V), dev); _want("row_kd", row_kd, torch.float32, (rows,), dev)
+    _want("t_val", t_val, torch.float32, (rows, K), dev); _want("t_idx", t_idx, torch.int32, (rows, K), dev)
+    if target is not None:
+        _want("target", target, torch.int32, (rows,), dev)
+    if row_ce is not None:
+        _want("row_ce", row_ce, torch.float32, (rows,), dev)
+    if dlogits is not None:
+        _want("dlogits", dlogits, torch.bfloat16, (rows, V), dev)
     _chk(_L().mt_distill_topk(_p(logits), _p(target), _p(t_val), _p(t_idx), rows, V, K, tau, w_ce, w_kd, _p(row_ce),
                               _p(row_kd), _p(dlogits), _stream()))
 
@@ -207,19 +221,21 @@ def router_balance(logits, idx, valid, S, alpha, z_coef, loss, counts, prob, dlo
     probabilities per group and expert, gradient of the logits
     (mt_router_balance).  valid and dlogits may be None."""
     import torch
-    from . import MtError
     T, E = logits.shape
     k = idx.shape[1]
     if S < 1 or T % S:
-        raise MtError(-1, f"{T} tokens are not groups of {S}")
-    _want("logits", logits, torch.float32, (T, E)); _want("idx", idx, torch.int32, (T, k))
-    _want("valid", valid, torch.uint8, (T,), True); _want("loss", loss, torch.float32, (2,))
-    _want("counts", counts, torch.int32, (T // S, E)); _want("prob", prob, torch.float32, (T // S, E))
-    _want("dlogits", dlogits, torch.bfloat16, (T, E), True)
-    _want_scratch(scratch, router_balance_scratch_bytes(T, S, E))
+        _refuse(f"{T} tokens are not groups of {S}")
+    G = T // S
+    dev = _device("logits", logits)
+    _want("logits", logits, torch.float32, (T, E), dev); _want("idx", idx, torch.int32, (T, k), dev)
+    _want("loss", loss, torch.float32, (2,), dev); _want("counts", counts, torch.int32, (G, E), dev)
+    _want("prob", prob, torch.float32, (G, E), dev)
+    if valid is not None:
+        _want("valid", valid, torch.uint8, (T,), dev)
+    if dlogits is not None:
+        _want("dlogits", dlogits, torch.bfloat16, (T, E), dev)
     _chk(_L().mt_router_balance(_p(logits), _p(idx), _p(valid), T, S, E, k, alpha, z_coef, _p(loss), _p(counts),
-                                _p(prob), _p(dlogits), _p(scratch), scratch.numel() * scratch.element_size(),
-                                _stream()))
+                                _p(prob), _p(dlogits), _p(scratch), _scratch(scratch, dev), _stream()))
 
 
 def moe_scratch_bytes(T, H, E, k, Fe):
