@@ -114,6 +114,8 @@ struct Params {
   int ngrp;
   int grp_e[MAX_EXPERT_GROUPS], grp_k0[MAX_EXPERT_GROUPS], grp_nk[MAX_EXPERT_GROUPS];
   SoftmaxPieces sp;   // softmax epilogue (gemm_softmax_pieces)
+  CUtensorMap td[2];  // D of each group, for the gradient epilogue's stores
+  int store[2];       // whether the group's D goes through td (a plain BF16 result)
 };
 
 __device__ __forceinline__ uint32_t su32(const void* p) {
@@ -198,6 +200,26 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// The same load without the wait, and the wait that hands over two of them
+// (the registers pass through it, so that nothing reads them before).
+__device__ __forceinline__ void tmem_ld32_nw(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld2(uint32_t (&a)[32], uint32_t (&b)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(a[i]), "+r"(b[i]));
 }
 
 // Shared-memory matrix descriptor (tcgen05 format): start address, leading
@@ -304,82 +326,146 @@ __device__ __forceinline__ void epi_store(const Epi& e, int row, int col, const 
   }
 }
 
-// Softmax epilogue of one row of a 256-column piece of logits (columns col0 ..
-// col0 + 255 of N, in TMEM from taddr on): m = the row's largest logit of the
-// piece, s = sum exp(z - m) over its columns but the target's (which the join
-// adds from zt, so that 1 - p of a confident row is a sum and no difference),
-// both from the FP32 accumulators, to stat[row][piece]; the target's logit, if
-// it lies in the piece, to zt; if wanted, fp16(2^15 exp(z - m)) to E (11 bits
-// down to 20 nats below the piece's maximum; BF16 would round every gradient
-// element a second time as coarsely as the first).  Two passes over the
-// accumulator, since m has to be known before the first exponential: reading
-// TMEM twice costs less than rescaling, and the epilogue hides behind the next
-// tile's MMAs.  All lanes take part in the loads; rows >= M store nothing.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"((uint64_t)map),
+               "r"(x), "r"(y), "r"(su32(src))
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void store_wait_read() {  // at most N of this thread's stores still read shared memory
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// 64 columns of a warp's 32 rows, 16 bits each, to global memory: through one
+// of the warp's two 4 KB buffers (rows of 128 bytes in the 128-byte swizzle, so
+// that neither side meets a bank twice) and out by TMA, which writes whole
+// lines and leaves out what lies beyond the matrix.  Straight from registers,
+// each lane writing 16-byte pieces of its own row, a 256 x 256 tile of short
+// sums took 6 us, more than its main loop.  pack(h, i): the i-th 8 values of
+// half h as 16 bytes.
+template <typename F>
+__device__ __forceinline__ void store_cols64(const CUtensorMap* map, int col, int row0, uint8_t* buf, int lane,
+                                             int& turn, F pack) {
+  uint8_t* b = buf + (turn & 1) * 4096;
+  if (lane == 0) store_wait_read<1>();  // the store before last has left this buffer
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4*>(b + lane * 128 + (((h * 4 + i) ^ (lane & 7)) << 4)) = pack(h, i);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0) {
+    tma_store(map, b, col, row0);
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+  ++turn;
+}
+
+// Gradient epilogue of one warp's 32 rows and 128 columns of a tile: alpha acc
+// in BF16.  The TMEM loads of the next 64 columns are on their way while these
+// are packed.
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, float alpha, int row0, int col0, int M, int N,
+                                           uint32_t taddr, uint8_t* buf, int lane, int& turn) {
+  if (row0 >= M || col0 >= N) return;  // warp-uniform
+  uint32_t r[2][2][32];
+  tmem_ld32_nw(taddr, r[0][0]);
+  tmem_ld32_nw(taddr + 32, r[0][1]);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    tmem_wait_ld2(r[c][0], r[c][1]);
+    if (col0 + c * 64 >= N) break;
+    if (c == 0) {
+      tmem_ld32_nw(taddr + 64, r[1][0]);
+      tmem_ld32_nw(taddr + 96, r[1][1]);
+    }
+    store_cols64(map, col0 + c * 64, row0, buf, lane, turn, [&](int h, int i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = pack_bf16(__uint_as_float(r[c][h][8 * i + 2 * k]) * alpha, __uint_as_float(r[c][h][8 * i + 2 * k + 1]) * alpha);
+      return make_uint4(w[0], w[1], w[2], w[3]);
+    });
+  }
+}
+
+// Softmax epilogue of one row of a piece of 128 columns of logits (columns col0
+// .. of N, in TMEM from taddr on): m = the row's largest logit of the piece, s =
+// sum exp(z - m) over its columns but the target's (which the join adds from
+// zt, so that 1 - p of a confident row is a sum and no difference), both from
+// the FP32 accumulators, to stat[row][piece]; the target's logit, if it lies in
+// the piece, to zt; if wanted, fp16(2^15 exp(z - m)) to E (11 bits down to 20
+// nats below the piece's maximum; BF16 would round every gradient element a
+// second time as coarsely as the first).  The piece is held in registers
+// between the maximum and the exponentials.  Bound by the four SM quarters'
+// issue slots (about 6 a value), hidden behind the next tile's MMAs from H of
+// about 700 on.  All lanes take part in the loads; rows >= M store nothing.
 template <bool STORE>
-__device__ __forceinline__ void softmax_piece(const SoftmaxPieces& sp, int row, int M, int N, int col0,
-                                              uint32_t taddr) {
+__device__ __forceinline__ void softmax_piece(const SoftmaxPieces& sp, const CUtensorMap* map, int row, int lane, int M,
+                                              int N, int col0, uint32_t taddr, uint8_t* buf, int& turn) {
+  if (row - lane >= M || col0 >= N) return;  // warp-uniform
   const bool live = row < M;
   const int tgt = live ? sp.target[row] : -1;
-  float m = -INFINITY;
-#pragma unroll 1
-  for (int c = 0; c < BN / 32; ++c) {
-    const int col = col0 + c * 32;
-    if (col >= N) break;  // warp-uniform
-    uint32_t r[32];
-    tmem_ld32(taddr + (uint32_t)(c * 32), r);
-    if (__any_sync(0xffffffffu, tgt >= col && tgt < col + 32 && tgt < N)) {  // once per row and pass over V
+  uint32_t r[4][32];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_ld32_nw(taddr + (uint32_t)(c * 32), r[c]);
+  tmem_wait_ld2(r[0], r[1]);
+  tmem_wait_ld2(r[2], r[3]);
+  const int left = N - col0;  // columns from here to the end
+  if (left < 128) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (tgt == col + i && tgt < N) sp.zt[row] = __uint_as_float(r[i]);
-    }
-    if (col + 32 <= N) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) m = fmaxf(m, __uint_as_float(r[i]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (col + i < N) m = fmaxf(m, __uint_as_float(r[i]));
-    }
+        if (c * 32 + i >= left) r[c][i] = 0xff800000u;  // -inf
   }
-  // every logit -inf (or NaN): the reference 0 leaves exp(z) = 0 (or NaN)
-  const float ref = m == -INFINITY ? 0.f : m;
-  float s0 = 0.f, s1 = 0.f;
-#pragma unroll 1
-  for (int c = 0; c < BN / 32; ++c) {
-    const int col = col0 + c * 32;
-    if (col >= N) break;
-    uint32_t r[32];
-    tmem_ld32(taddr + (uint32_t)(c * 32), r);
-    float v[32];
-    // z - m first, exact for the terms that count, then the factor log2(e): a
-    // fused z log2(e) - m log2(e) would lose digits where |z| is large
+  const int ti = tgt - col0;  // the target's place in the piece
+  const bool mine = ti >= 0 && ti < 128 && tgt < N;
+  float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = exp2_approx(fmaf(__uint_as_float(r[i]) - ref, kLog2e, 15.f));
-    if (col + 32 > N) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (col + i >= N) v[i] = 0.f;
-    }
-    if (__any_sync(0xffffffffu, tgt >= col && tgt < col + 32)) {  // the target's own column is overwritten by the join
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (tgt == col + i) v[i] = 0.f;
-    }
+  for (int c = 0; c < 4; ++c)
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-      s0 += v[i];
-      s1 += v[i + 1];
+      m0 = fmaxf(m0, __uint_as_float(r[c][i]));
+      m1 = fmaxf(m1, __uint_as_float(r[c][i + 1]));
     }
-    if (STORE && live) {
-      uint4* p = reinterpret_cast<uint4*>(sp.E + (int64_t)row * sp.ldE + col);
+  const float m = fmaxf(m0, m1);
+  // every logit -inf (or NaN): the reference 0 leaves exp(z) = 0 (or NaN)
+  const float ref = m == -INFINITY ? 0.f : m;
+  if (__any_sync(0xffffffffu, mine)) {  // once per row and pass over V
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (col + 8 * i < N)  // ldE is N rounded up to 8 columns at least: a started vector fits the row
-          p[i] = make_uint4(pack_half(v[8 * i], v[8 * i + 1]), pack_half(v[8 * i + 2], v[8 * i + 3]),
-                            pack_half(v[8 * i + 4], v[8 * i + 5]), pack_half(v[8 * i + 6], v[8 * i + 7]));
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (mine && ti == c * 32 + i) {
+          sp.zt[row] = __uint_as_float(r[c][i]);
+          r[c][i] = 0xff800000u;  // out of the sum; the join writes its gradient
+        }
+  }
+  float s0 = 0.f, s1 = 0.f;
+  // z - m first, exact for the terms that count, then the factor log2(e): a
+  // fused z log2(e) - m log2(e) would lose digits where |z| is large
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float a = exp2_approx(fmaf(__uint_as_float(r[c][i]) - ref, kLog2e, 15.f));
+      const float b = exp2_approx(fmaf(__uint_as_float(r[c][i + 1]) - ref, kLog2e, 15.f));
+      s0 += a;
+      s1 += b;
+      if (STORE) r[c][i >> 1] = pack_half(a, b);
+    }
+  if (live) sp.stat[(int64_t)row * sp.npieces + col0 / 128] = make_float2(ref, (s0 + s1) * 0x1p-15f);
+  if (STORE) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      if (c * 64 >= left) break;
+      store_cols64(map, col0 + c * 64, row - lane, buf, lane, turn, [&](int h, int i) {
+        return make_uint4(r[2 * c + h][4 * i], r[2 * c + h][4 * i + 1], r[2 * c + h][4 * i + 2], r[2 * c + h][4 * i + 3]);
+      });
     }
   }
-  if (live) sp.stat[(int64_t)row * sp.npieces + col0 / BN] = make_float2(ref, (s0 + s1) * 0x1p-15f);
 }
 
 // Producer side of one output tile: its K-blocks into the shared-memory ring.
@@ -666,6 +752,25 @@ __host__ __device__ constexpr int p_stages() {
   return NW == 1 ? P_STAGES : 4;
 }
 static_assert(4 * (PA_BYTES + 2 * PB_BYTES) == P_STAGES * P_STAGE_BYTES, "wide and narrow rings share one layout");
+// The kernels of the linear cross-entropy (EPI 1 to 3) have eight epilogue
+// warps, two per TMEM lane quarter with 128 of a tile's 256 columns each, and
+// those that write through shared memory (EPI 2 and 3) two 4 KB buffers a warp
+// and a ring of five stages to make room for them.
+constexpr int P_BUF_BYTES = 8 * 2 * 4096;
+template <int EPI>
+__host__ __device__ constexpr int p_threads() {
+  return EPI == 0 ? THREADS : THREADS + 128;
+}
+template <int NW, int EPI>
+__host__ __device__ constexpr int p_ring() {
+  return EPI >= 2 ? 5 : p_stages<NW>();
+}
+template <int EPI>
+__host__ __device__ constexpr int p_smem() {
+  // 1024 to align the ring, 1024 for the barriers (so that the buffers are aligned too)
+  return EPI >= 2 ? 5 * P_STAGE_BYTES + 2048 + P_BUF_BYTES : P_SMEM_BYTES;
+}
+static_assert(p_smem<3>() <= 232448, "shared memory of a block");
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -727,7 +832,7 @@ __device__ __forceinline__ void pair_tile_mn(int tile, const Epi& e, int& tm, in
 
 // Producer side of one pair tile: this CTA's halves of A and B, K block by K
 // block (B: one 128-row block per 256 columns of the tile, 256 apart).
-template <bool A_MN, bool B_MN, int NW>
+template <bool A_MN, bool B_MN, int NW, int ST>
 __device__ __forceinline__ bool produce_pair_tile(const CUtensorMap* tmA, const CUtensorMap* tmB, int arow, int brow,
                                                   int nk, uint8_t* sA, uint8_t* sB, uint64_t* full, uint64_t* empty,
                                                   bool leader, int& stage, uint32_t& phase, volatile int* abort_flag,
@@ -758,7 +863,7 @@ __device__ __forceinline__ bool produce_pair_tile(const CUtensorMap* tmA, const 
     }
     inflight_mask |= 1u << stage;
     inflight_parity = (inflight_parity & ~(1u << stage)) | (phase << stage);
-    if (++stage == p_stages<NW>()) {
+    if (++stage == ST) {
       stage = 0;
       phase ^= 1;
     }
@@ -769,7 +874,7 @@ __device__ __forceinline__ bool produce_pair_tile(const CUtensorMap* tmA, const 
 // MMA side of one pair tile (the even CTA's issuing thread): per K step one
 // M = 256, N = 256 MMA per 256 columns of the tile, into accumulator columns
 // 256 w .. 256 w + 255.
-template <bool A_MN, bool B_MN, int NW>
+template <bool A_MN, bool B_MN, int NW, int ST>
 __device__ __forceinline__ bool mma_pair_tile(uint32_t d, int nk, uint8_t* sA, uint8_t* sB, uint64_t* full,
                                               uint64_t* empty, int& stage, uint32_t& phase, volatile int* abort_flag) {
   constexpr uint32_t ID = idesc_pair(A_MN, B_MN);
@@ -788,7 +893,7 @@ __device__ __forceinline__ bool mma_pair_tile(uint32_t d, int nk, uint8_t* sA, u
       }
     }
     tc_commit_pair(&empty[stage]);  // the stage is free in both CTAs once these MMAs are done
-    if (++stage == p_stages<NW>()) {
+    if (++stage == ST) {
       stage = 0;
       phase ^= 1;
     }
@@ -797,9 +902,8 @@ __device__ __forceinline__ bool mma_pair_tile(uint32_t d, int nk, uint8_t* sA, u
 }
 
 constexpr int P_TRING = 4;  // tile ids in flight between the pair's producer and its consumers
-// consumers that release a tile-id slot on the even CTA: its MMA thread, the odd CTA's
-// producer and lane 0 of the four epilogue warps of each CTA
-constexpr int P_TID_CONSUMERS = 1 + 1 + 2 * 4;
+// (a slot is released on the even CTA by its MMA thread, the odd CTA's producer and lane 0
+// of every epilogue warp of each CTA)
 
 __device__ __forceinline__ bool mbar_test_cl(uint64_t* b, uint32_t parity) {
   uint32_t ok;
@@ -826,6 +930,11 @@ __device__ __forceinline__ void st_cluster_s32(uint32_t addr, int v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// A kernel launched with programmatic serialisation sets itself up while the
+// one before it runs, and sees that one's writes after dep_wait().
+__device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // The K blocks of a tile of group `e`: all of them, or with EPI 3 one run of a
 // split sum, `tile` then becoming the tile's index within its run.
 template <int EPI>
@@ -845,12 +954,16 @@ __device__ __forceinline__ void tile_run(const Epi& e, int& tile, int& run, int&
 // narrow (256 x 256) tile, without and with the exponentials stored; 3: the
 // plain epilogue with a factor, and split sums (Epi::alpha, ksplit).
 template <int NG, bool A0, bool B0, bool A1, bool B1, int NW = 1, int EPI = 0>
-__global__ void __launch_bounds__(THREADS, 1) gemm_pair_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(p_threads<EPI>(), 1) gemm_pair_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int ST = p_ring<NW, EPI>();
+  constexpr int EW = EPI == 0 ? 4 : 8;            // epilogue warps
+  constexpr int EC = BN * NW / (EPI == 0 ? 1 : 2);  // columns of a tile each of them takes
+  constexpr int RING = EPI >= 2 ? 5 * P_STAGE_BYTES : P_STAGES * P_STAGE_BYTES;
   uint8_t* sA = smem;
-  uint8_t* sB = smem + p_stages<NW>() * PA_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + P_STAGES * P_STAGE_BYTES);
+  uint8_t* sB = smem + ST * PA_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING);
   uint64_t* empty = full + P_STAGES;
   uint64_t* tfull = empty + P_STAGES;
   uint64_t* tempty = tfull + 2;
@@ -874,11 +987,11 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_pair_kernel(const __grid_cons
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * 128);  // the epilogue threads of both CTAs (the even CTA's counts)
+      mbar_init(&tempty[a], 2 * 32 * EW);  // the epilogue threads of both CTAs (the even CTA's counts)
     }
     for (int r = 0; r < P_TRING; ++r) {
       mbar_init(&tid_full[r], 1);
-      mbar_init(&tid_empty[r], P_TID_CONSUMERS);  // the even CTA's counts
+      mbar_init(&tid_empty[r], 1 + 1 + 2 * EW);  // the even CTA's counts
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -913,6 +1026,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_pair_kernel(const __grid_cons
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
+      if (EPI != 0) dep_wait();
       const int tickets = (num_tiles > ncl ? num_tiles - ncl : 0) + ncl;
       int ahead = -1;  // the ticket drawn one tile ahead (its latency hides behind the current tile's loads)
       for (int i = 0; ok && !p.stall; ++i) {
@@ -956,18 +1070,19 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_pair_kernel(const __grid_cons
         if (NG == 1 || tile < split) {
           tile_run<EPI>(p.e[0], tile, run, kb0, nk);
           pair_tile_mn(tile, p.e[0], tm, tn);
-          ok = produce_pair_tile<A0, B0, NW>(&p.ta[0], &p.tb[0], tm * 2 * BM + (int)rank * BM,
+          ok = produce_pair_tile<A0, B0, NW, ST>(&p.ta[0], &p.tb[0], tm * 2 * BM + (int)rank * BM,
                                              tn * BN * NW + (int)rank * (BN / 2), nk, sA, sB, full, empty, leader,
                                              stage, phase, abort_flag, inflight_mask, inflight_parity, kb0);
         } else {
           tile -= split;
           tile_run<EPI>(p.e[1], tile, run, kb0, nk);
           pair_tile_mn(tile, p.e[1], tm, tn);
-          ok = produce_pair_tile<A1, B1, NW>(&p.ta[1], &p.tb[1], tm * 2 * BM + (int)rank * BM,
+          ok = produce_pair_tile<A1, B1, NW, ST>(&p.ta[1], &p.tb[1], tm * 2 * BM + (int)rank * BM,
                                              tn * BN * NW + (int)rank * (BN / 2), nk, sA, sB, full, empty, leader,
                                              stage, phase, abort_flag, inflight_mask, inflight_parity, kb0);
         }
       }
+      if (EPI != 0) dep_launch();  // the next kernel may set itself up while the last tiles are finished
       if (!ok) fail(abort_flag, 1);
     }
   } else if (warp == 1) {
@@ -996,11 +1111,11 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_pair_kernel(const __grid_cons
         int run, kb0, nk;
         if (NG == 1 || tile < split) {
           tile_run<EPI>(p.e[0], tile, run, kb0, nk);
-          ok = mma_pair_tile<A0, B0, NW>(d, nk, sA, sB, full, empty, stage, phase, abort_flag);
+          ok = mma_pair_tile<A0, B0, NW, ST>(d, nk, sA, sB, full, empty, stage, phase, abort_flag);
         } else {
           tile -= split;
           tile_run<EPI>(p.e[1], tile, run, kb0, nk);
-          ok = mma_pair_tile<A1, B1, NW>(d, nk, sA, sB, full, empty, stage, phase, abort_flag);
+          ok = mma_pair_tile<A1, B1, NW, ST>(d, nk, sA, sB, full, empty, stage, phase, abort_flag);
         }
         if (!ok) break;
         tc_commit_pair(&tfull[acc]);  // both CTAs' epilogues may read their rows
@@ -1011,6 +1126,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_pair_kernel(const __grid_cons
     const int q = warp & 3;  // this warp may read TMEM lanes 32q .. 32q+31
     const int row_in_tile = q * 32 + lane;
     const uint32_t tempty_lead[2] = {cluster_addr(&tempty[0], 0), cluster_addr(&tempty[1], 0)};
+    const int half = (warp - 2) >> 2;  // 0, or for eight warps which columns of the tile
+    uint8_t* store_buf = smem + RING + 1024 + (warp - 2) * 8192;  // EPI >= 2; after the barriers' 1024 bytes
+    int store_turn = 0;
+    if (EPI != 0) dep_wait();  // nothing of the kernels before may still be read, or not yet written
     bool ok = true;
     for (int it = 0;; ++it) {
       const int slot = it % P_TRING;
@@ -1041,19 +1160,30 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_pair_kernel(const __grid_cons
       }
       const int row = tm * 2 * BM + (int)rank * BM + row_in_tile;
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
-      if constexpr (EPI == 1 || EPI == 2) softmax_piece<EPI == 2>(p.sp, row, e.M, e.N, tn * BN, taddr);
-      else for (int c = 0; c < BN * NW / 32; ++c) {
-        uint32_t r[32];
-        tmem_ld32(taddr + (uint32_t)(c * 32), r);
-        const int col = tn * BN * NW + c * 32;
-        if (row < e.M && col < e.N) {
-          if constexpr (EPI == 3) epi_store<true>(er, row, col, r);
-          else epi_store(e, row, col, r);
+      const int col0 = tn * BN * NW + half * EC;
+      const uint32_t tcol = taddr + (uint32_t)(half * EC);
+      if constexpr (EPI == 1 || EPI == 2) {
+        softmax_piece<EPI == 2>(p.sp, &p.td[0], row, lane, e.M, e.N, col0, tcol, store_buf, store_turn);
+      } else {
+        const int grp = (NG == 1 || tile < split) ? 0 : 1;
+        if (EPI == 3 && p.store[grp]) {
+          store_tile(&p.td[grp], e.alpha, row - lane, col0, e.M, e.N, tcol, store_buf, lane, store_turn);
+        } else {
+          for (int c = 0; c < EC / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld32(tcol + (uint32_t)(c * 32), r);
+            const int col = col0 + c * 32;
+            if (row < e.M && col < e.N) {
+              if constexpr (EPI == 3) epi_store<true>(er, row, col, r);
+              else epi_store(e, row, col, r);
+            }
+          }
         }
       }
       tc_fence_before();
       mbar_arrive_remote(tempty_lead[acc]);  // the even CTA counts both CTAs' epilogues
     }
+    if (EPI >= 2 && lane == 0) store_wait_read<0>();
     if (!ok && lane == 0) fail(abort_flag, 3);
   }
 
@@ -1125,13 +1255,17 @@ void init_once() {
                                 (const void*)gemm_pair_kernel<1, true, false, false, false, 2>,
                                 (const void*)gemm_pair_kernel<1, true, true, false, false, 2>,
                                 (const void*)gemm_pair_kernel<2, true, true, false, true, 2>,
-                                (const void*)gemm_pair_kernel<2, false, true, true, true, 1, 3>,
-                                (const void*)gemm_pair_kernel<1, false, true, false, false, 1, 3>,
-                                (const void*)gemm_pair_kernel<1, true, true, false, false, 1, 3>,
-                                (const void*)gemm_pair_kernel<1, false, false, false, false, 1, 1>,
-                                (const void*)gemm_pair_kernel<1, false, false, false, false, 1, 2>};
+                                (const void*)gemm_pair_kernel<1, false, false, false, false, 1, 1>};
   for (const void* k : pair_kernels) {
     const cudaError_t a = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM_BYTES);
+    if (a != cudaSuccess) g_init_err = a;
+  }
+  const void* loss_kernels[] = {(const void*)gemm_pair_kernel<1, false, false, false, false, 1, 2>,
+                                (const void*)gemm_pair_kernel<2, false, true, true, true, 1, 3>,
+                                (const void*)gemm_pair_kernel<1, false, true, false, false, 1, 3>,
+                                (const void*)gemm_pair_kernel<1, true, true, false, false, 1, 3>};
+  for (const void* k : loss_kernels) {
+    const cudaError_t a = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, p_smem<3>());
     if (a != cudaSuccess) g_init_err = a;
   }
   // pairs resident at once (an SM pair shares a TPC; the count can be below SMs / 2)
@@ -1259,20 +1393,22 @@ int pair_band(int K, int pairs) {
 }
 
 template <int NG, bool A0, bool B0, bool A1, bool B1, int NW = 1, int EPI = 0>
-cudaError_t launch_pair_kernel(const Params& p, int tiles, cudaStream_t s) {
+cudaError_t launch_pair_kernel(const Params& p, int tiles, cudaStream_t s, bool dependent = false) {
   const int clusters = tiles < g_pair_clusters ? tiles : g_pair_clusters;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(2 * (clusters > 0 ? clusters : 1)));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = P_SMEM_BYTES;
+  cfg.blockDim = dim3(p_threads<EPI>());
+  cfg.dynamicSmemBytes = p_smem<EPI>();
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = dependent ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<NG, A0, B0, A1, B1, NW, EPI>, p);
 }
 
@@ -1426,15 +1562,17 @@ cudaError_t gemm_pair(const GemmArgs& g0, const GemmArgs& g1, cudaStream_t s) {
 }
 
 cudaError_t gemm_softmax_pieces(const bf16* A, const bf16* B, int M, int N, int K, const SoftmaxPieces& sp,
-                                int* tile_ctr, cudaStream_t s) {
+                                int* tile_ctr, bool dependent, cudaStream_t s) {
   std::call_once(g_once, init_once);
   if (g_init_err != cudaSuccess) return g_init_err;
-  if (M <= 0 || N <= 0 || K <= 0 || K % 8 || !al16(A) || !al16(B) || !sp.stat || !sp.zt || !sp.target || !tile_ctr)
+  if (M <= 0 || N <= 0 || K <= 0 || K % 8 || !al16(A) || !al16(B) || !sp.stat || !sp.zt || !sp.target)
     return cudaErrorInvalidValue;
-  if (sp.npieces != (N + BN - 1) / BN || (sp.E && (!al16(sp.E) || sp.ldE % 8 || sp.ldE < N))) return cudaErrorInvalidValue;
+  if (sp.npieces != (N + 127) / 128 || (sp.E && (!al16(sp.E) || sp.ldE % 8 || sp.ldE < N))) return cudaErrorInvalidValue;
   Params p;
   std::memset(&p, 0, sizeof p);
   if (!make_map(&p.ta[0], A, M, K, K, BM) || !make_map(&p.tb[0], B, N, K, K, BN / 2)) return cudaErrorInvalidValue;
+  // E in 16-bit words, 64 columns by a warp's 32 rows
+  if (sp.E && !make_map(&p.td[0], reinterpret_cast<const bf16*>(sp.E), M, N, sp.ldE, 32)) return cudaErrorInvalidValue;
   fill_epi(&p.e[0], M, N, K, nullptr, 0);
   p.e[0].group_m = pair_band(K, g_pair_clusters);
   p.ngroups = 1;
@@ -1442,15 +1580,15 @@ cudaError_t gemm_softmax_pieces(const bf16* A, const bf16* B, int M, int N, int 
   p.tile_ctr = tile_ctr;
   p.sp = sp;
   p.stall = gemm_stall_take();
-  const cudaError_t r = sp.E ? launch_pair_kernel<1, false, false, false, false, 1, 2>(p, p.tile_start[1], s)
-                             : launch_pair_kernel<1, false, false, false, false, 1, 1>(p, p.tile_start[1], s);
+  const cudaError_t r = sp.E ? launch_pair_kernel<1, false, false, false, false, 1, 2>(p, p.tile_start[1], s, dependent)
+                             : launch_pair_kernel<1, false, false, false, false, 1, 1>(p, p.tile_start[1], s, dependent);
   return r != cudaSuccess ? r : cudaGetLastError();
 }
 
 cudaError_t gemm_grads(const GradArgs& g, cudaStream_t s) {
   std::call_once(g_once, init_once);
   if (g_init_err != cudaSuccess) return g_init_err;
-  if (!g.tile_ctr || !(g.dgrad || g.wgrad) || (g.dgrad && (g.dgrad->a_mn || !g.dgrad->b_mn)) ||
+  if (!(g.dgrad || g.wgrad) || (g.dgrad && (g.dgrad->a_mn || !g.dgrad->b_mn)) ||
       (g.wgrad && (!g.wgrad->a_mn || !g.wgrad->b_mn)))
     return cudaErrorInvalidValue;
   Params p;
@@ -1480,14 +1618,18 @@ cudaError_t gemm_grads(const GradArgs& g, cudaStream_t s) {
       if (ep.ksplit != g.ksplit) return cudaErrorInvalidValue;
       ep.slab = (int64_t)ep.M * ep.N;
     }
+    if (w.D && !w.acc_mode && !w.R) {  // a plain result: box of 64 columns by a warp's 32 rows
+      if (!make_map(&p.td[i], w.D, w.M, w.N, w.ldd, 32)) return cudaErrorInvalidValue;
+      p.store[i] = 1;
+    }
     p.tile_start[i + 1] = p.tile_start[i] + (ep.M + 2 * BM - 1) / (2 * BM) * ep.tiles_n * ep.ksplit;
   }
   p.tile_ctr = g.tile_ctr;
   p.stall = gemm_stall_take();
   const int tiles = p.tile_start[p.ngroups];
-  const cudaError_t r = p.ngroups == 2 ? launch_pair_kernel<2, false, true, true, true, 1, 3>(p, tiles, s)
-                        : g.dgrad      ? launch_pair_kernel<1, false, true, false, false, 1, 3>(p, tiles, s)
-                                       : launch_pair_kernel<1, true, true, false, false, 1, 3>(p, tiles, s);
+  const cudaError_t r = p.ngroups == 2 ? launch_pair_kernel<2, false, true, true, true, 1, 3>(p, tiles, s, true)
+                        : g.dgrad      ? launch_pair_kernel<1, false, true, false, false, 1, 3>(p, tiles, s, true)
+                                       : launch_pair_kernel<1, true, true, false, false, 1, 3>(p, tiles, s, true);
   return r != cudaSuccess ? r : cudaGetLastError();
 }
 
@@ -1508,6 +1650,9 @@ cudaError_t kernel_error_read(int* code, int clear) {
   }
   int a = 0;
   e = attention_error_read(&a, clear);
+  if (*code == 0) *code = a;
+  if (e != cudaSuccess) return e;
+  e = loss_error_read(&a, clear);
   if (*code == 0) *code = a;
   return e;
 }

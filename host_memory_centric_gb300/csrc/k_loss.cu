@@ -9,6 +9,8 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 namespace mt {
 namespace {
 
@@ -63,6 +65,11 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   return t;
 }
 
+// A kernel launched with programmatic serialisation may start while the one
+// before it runs; it sees that one's writes after dep_wait().
+__device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------------------ linear cross-entropy
 // One block per row: joins the row's pieces (m_p, s_p), whose sums leave the
 // target out, with M = max m_p:
@@ -70,7 +77,7 @@ __device__ __forceinline__ float block_max(float v, float* red) {
 //   loss = (M - z_target) + log S,
 // and, with E, turns the stored fp16 2^15 exp(z - m_p) into the logits'
 // gradient in BF16 in place: d = exp(z - m_p) exp(m_p - M) / S, one factor per
-// piece of 256 columns, and d = -rest / S (= p - 1) at the target, so that loss
+// piece of 128 columns, and d = -rest / S (= p - 1) at the target, so that loss
 // and gradient of a confident row (p near 1) keep their digits.  The factor g
 // of the gradients waits for the products' FP32 results: rounded here, g (p - 1)
 // of most rows would be off by the same amount, and the errors would add up.
@@ -84,13 +91,15 @@ __global__ void __launch_bounds__(JOIN_THREADS) ce_join_k(const float2* __restri
                                                           float* __restrict__ row_loss, uint16_t* __restrict__ E,
                                                           int64_t ldE) {
   __shared__ float red[JOIN_THREADS / 32];
+  dep_launch();
+  dep_wait();
   const int64_t row = blockIdx.x;
   const int tgt = target[row];
   const bool has = tgt >= 0 && tgt < V;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint4* e = reinterpret_cast<uint4*>(E + row * ldE);
   const int nvec = (V + 7) / 8, step = 32 * (JOIN_THREADS / 32) * (int)gridDim.y;
-  const int first = ((int)blockIdx.y * (JOIN_THREADS / 32) + warp) * 32 + lane;  // a warp's 32 vectors are one piece
+  const int first = ((int)blockIdx.y * (JOIN_THREADS / 32) + warp) * 32 + lane;
   if (!has) {
     if (threadIdx.x == 0 && blockIdx.y == 0) row_loss[row] = 0.f;
     if (E)
@@ -117,7 +126,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) ce_join_k(const float2* __restri
       const int w = v + u * step;
       if (w < nvec) {
         q[u] = e[w];
-        f[u] = st[w >> 5].x;
+        f[u] = st[w >> 4].x;
       }
     }
 #pragma unroll
@@ -147,6 +156,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) ce_join_k(const float2* __restri
 __global__ void __launch_bounds__(256) ce_add_runs_k(const float4* __restrict__ slabs, int64_t n4, int runs, float g,
                                                      uint2* __restrict__ dh) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  dep_launch();
+  dep_wait();
   if (i >= n4) return;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -186,11 +197,6 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
 __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-// A kernel launched with programmatic serialisation may start while the one
-// before it runs; it sees that one's writes after dep_wait().
-__device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -205,17 +211,19 @@ __device__ __forceinline__ float ex2(float x) {
 //   dz_v = w_ce (softmax(z)_v - [v = target]) + w_kd / tau (p_v - sum_{i_j = v} q_j).
 // Bound by HBM: the row has to be known before its first gradient element, so
 // it is read once and kept: a cluster of 1 to 8 blocks holds a row in
-// registers, NV 16-byte vectors a thread, all of them loaded before the first
-// is used.  Every thread sums exp(z - m) around its own maximum m at both
-// temperatures; each warp sends its joined (m, s1, st) to every block of the
-// cluster through distributed shared memory, and after the one barrier every
-// warp joins them all; then the gradient is computed from the same registers.
-// The last warp of a block holds no part of the row: it works out the
-// teacher's distribution, whose dependent loads would otherwise stand before
-// the barrier.  The at most K + 1 columns with a teacher entry or the target
-// are written again from their FP32 values by the block that holds them, each
-// by one thread, so that no element is rounded twice and an id that appears in
-// several slots gets the sum of their q, in slot order.
+// registers, NV 16-byte vectors a thread.  The clusters are resident and take
+// every n-th row; a bulk copy brings a block's part of its next row to shared
+// memory while this one is worked on, so that no thread waits for HBM.  Every
+// warp sums exp(z - m) around its own maximum m at both temperatures and sends
+// (m, s1, st) to every block of the cluster through distributed shared memory;
+// after the one barrier a row has every warp joins them all, and the gradient
+// is computed from the same registers.  The last warp of a block holds no part
+// of the row: it issues the copies, and works out the teacher's distribution,
+// whose dependent loads would otherwise stand before the barrier.  The at most
+// K + 1 columns with a teacher entry or the target are written again from their
+// FP32 values by the block that holds them, each by one thread, so that no
+// element is rounded twice and an id that appears in several slots gets the sum
+// of their q, in slot order.
 constexpr int KD_MAX_K = 1024;
 constexpr int KD_MAX_CLUSTER = 8;
 constexpr int KD_WIDE_NV = 18;
@@ -223,6 +231,8 @@ constexpr int KD_MAX_V = 524288;
 static_assert(KD_MAX_CLUSTER * 480 * KD_WIDE_NV * 8 >= KD_MAX_V, "the widest form holds the widest row");
 
 struct KdArgs {
+  int64_t rows;
+  int kcap;  // slots there is room for: K up to a power of two, at least 32
   const bf16* logits;
   const int32_t* target;
   const float* t_val;
@@ -233,7 +243,89 @@ struct KdArgs {
   bf16* dlogits;
 };
 
-__device__ __forceinline__ uint32_t bf16_bits(const bf16* p) { return *reinterpret_cast<const uint16_t*>(p); }
+// Two FP32 values in a register pair: one instruction for both
+// (fma / add / mul.f32x2), each rounded as the single form rounds it.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 wide2(uint32_t w) {  // the two BF16 values of a word
+  return pair2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ f32x2 ex2_2(f32x2 v) {
+  const float2 t = unpair2(v);
+  return pair2(ex2(t.x), ex2(t.y));
+}
+
+// A bounded wait of this file's kernels ran out (0: none did).
+__device__ int g_loss_error = 0;
+constexpr long long kWaitCycles = 4000000000LL;  // about 2 s at 2 GHz
+
+__device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(b)), "r"(n));
+}
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(su32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait; once one ran out (recorded in g_loss_error: the outputs are not
+// valid) this thread waits for nothing more, so that the kernel ends.
+__device__ __forceinline__ void mbar_wait(uint64_t* b, uint32_t parity, bool& failed) {
+  if (failed || mbar_test(b, parity)) return;
+  const long long t0 = clock64();
+  while (!mbar_test(b, parity)) {
+    if (clock64() - t0 > kWaitCycles) {
+      failed = true;
+      atomicCAS(&g_loss_error, 0, 4);
+      return;
+    }
+  }
+}
+// n bytes (a multiple of 16) from global to shared memory, both 16-byte
+// aligned; their arrival completes on the barrier
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t n, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(su32(dst)),
+               "l"(src), "r"(n), "r"(su32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void async_load4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(su32(dst)), "l"(src) : "memory");
+}
 
 // Blocks per SM that the registers are to allow: the row's 4 NV and about 36
 // more a thread, else the compiler keeps unpacked copies of the row (254 registers at NV = 12).
@@ -242,219 +334,294 @@ constexpr int kd_blocks() {
   return 65536 / (NT * (4 * NV + 36)) > 6 ? 6 : 65536 / (NT * (4 * NV + 36));
 }
 template <int NV, int NT>
+constexpr size_t kd_smem(int kcap) {
+  return (size_t)NV * (NT - 32) * 16 + (size_t)kcap * (2 * 4 + 2) * 4;
+}
+// TWO: both temperatures are summed (hard targets and tau != 1); else one
+// exponential serves both.  Exponentials are taken as 2^(z a - c) with a =
+// log2(e) or log2(e) / tau and the reference c = fl(m a) kept as it is rounded,
+// so that the fused product loses nothing.
+template <int NV, int NT, bool TWO>
 __global__ void __launch_bounds__(NT, kd_blocks<NV, NT>()) distill_k(const KdArgs a) {
   constexpr int DT = NT - 32, DW = DT / 32;  // threads and warps that hold the row
-  extern __shared__ __align__(16) float slots[];  // id [K4], y / tau - max [K4], q [K4], z at id [K4]; K4 = K up to 4s
-  __shared__ float peer[KD_MAX_CLUSTER * DW][3];
-  __shared__ float t_sum;                    // sum of the teacher's exponentials; 0: no teacher
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint4* buf = reinterpret_cast<uint4*>(smem);                       // [NV][DT]: this block's part of the next row
+  float* slots = reinterpret_cast<float*>(smem + NV * DT * 16);      // two rows' slots, used in turn
+  int* table = reinterpret_cast<int*>(slots + 2 * 4 * a.kcap);       // [2 kcap] ids seen, -1 free
+  __shared__ float peer[2][KD_MAX_CLUSTER * (DW + 1)][3];
+  __shared__ int s_tgt[2];       // the row's target, -1: none
+  __shared__ float s_zt[2];      // its logit
+  __shared__ int s_flags[2];     // 1: a teacher, 2: an id in several slots, 4: the target in a slot
+  __shared__ uint64_t full, empty;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int V = a.V, K = a.K, K4 = (K + 3) & ~3;
-  int* id = reinterpret_cast<int*>(slots);
-  float *y = slots + K4, *q = slots + 2 * K4, *zj = slots + 3 * K4;
+  const int V = a.V, K = a.K;
   const uint32_t rank = cluster_rank(), ncta = cluster_size();
-  const int64_t row = blockIdx.x / ncta;
-  const bf16* z = a.logits + row * V;
-  // 16-byte vectors of memory that the row touches; the first and last may hold
-  // elements of its neighbours, which are neither read nor written
-  const int skip = (int)((row * V) & 7);
-  const int nvec = (skip + V + 7) >> 3, per = (nvec + (int)ncta - 1) / (int)ncta;
-  const int v0 = (int)rank * per, v1 = min(nvec, v0 + per);
+  const int64_t first_row = blockIdx.x / ncta, stride = gridDim.x / ncta;
   const float it = 1.f / a.tau, itl = it * kLog2e;
-  const int tgt = a.target ? a.target[row] : -1;
-  const bool hard = tgt >= 0 && tgt < V;
-  // one exponential where one temperature is needed or both are the same
-  const bool two = hard && a.tau != 1.f;
-  const uint4* zv = reinterpret_cast<const uint4*>(z - skip);
-  uint4 r[NV];
-  float zt = 0.f;
+  constexpr float kLn2 = 0.6931471805599453f;
+  bool failed = false;
+  if (tid == 0) {
+    mbar_init(&full, 1);
+    mbar_init(&empty, DW);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  cluster_sync();  // the barriers are ready, and every block of the cluster has started
 
-  if (warp < DW) {
+  // the row in memory: up to 7 elements, whole 16-byte vectors, up to 7
+  // elements.  The vectors are shared out to the blocks; the elements at the
+  // ends belong to lanes of block 0's last warp.
+  int head, nvec, per;
+  auto place = [&](int64_t row) {
+    const int skip = (int)((row * V) & 7);
+    head = skip ? min(8 - skip, V) : 0;
+    nvec = (V - head) >> 3;
+    per = (nvec + (int)ncta - 1) / (int)ncta;
+  };
+  int tgt_next = -1;
+  auto fetch = [&](int64_t row, int par) {  // the last warp: start everything row `row` needs on its way
+    place(row);
+    if (lane == 0) {
+      const int n = min(nvec, ((int)rank + 1) * per) - (int)rank * per;
+      if (n > 0) {
+        mbar_expect_tx(&full, (uint32_t)n * 16);
+        bulk_load(buf, a.logits + row * V + head + (int64_t)rank * per * 8, (uint32_t)n * 16, &full);
+      } else {
+        mbar_arrive(&full);
+      }
+    }
+    float* sl = slots + par * 4 * a.kcap;
+    for (int j = lane; j < K; j += 32) {
+      async_load4(sl + j, a.t_idx + row * K + j);
+      async_load4(sl + a.kcap + j, a.t_val + row * K + j);
+    }
+    tgt_next = a.target ? a.target[row] : -1;
+  };
+  if (warp == DW && first_row < a.rows) fetch(first_row, 0);
+
+  int turn = 0;
+  for (int64_t row = first_row; row < a.rows; row += stride, ++turn) {
+    const int par = turn & 1;
+    int* id = reinterpret_cast<int*>(slots + par * 4 * a.kcap);
+    float *y = reinterpret_cast<float*>(id) + a.kcap, *q = y + a.kcap, *zj = q + a.kcap;
+    place(row);
+    const int v0 = (int)rank * per + tid, v1 = min(nvec, ((int)rank + 1) * per);
+    uint4 r[NV];
+    float ze = -INFINITY;  // an end element
+    int ie = -1;           // its index
+    float wm, s1, st, ysum = 0.f;
+
+    if (warp < DW) {
+      mbar_wait(&full, (uint32_t)par, failed);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int v = v0 + j * DT + tid, c = v * 8 - skip;
-      r[j] = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);  // -inf: no probability
-      if (v < v1) {
-        if (c >= 0 && c + 8 <= V) {
-          r[j] = zv[v];
-        } else {
-          uint32_t w[4];
+      for (int j = 0; j < NV; ++j) {
+        r[j] = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);  // -inf: no probability
+        if (v0 + j * DT < v1) r[j] = buf[j * DT + tid];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty);
+      // packed maxima: exact, and NaN passes by (it shows in the sums)
+      __nv_bfloat162 mx = __halves2bfloat162(__ushort_as_bfloat16(0xFF80), __ushort_as_bfloat16(0xFF80));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int e = c + 2 * k;
-            const uint32_t lo = e >= 0 && e < V ? bf16_bits(z + e) : 0xFF80u;
-            const uint32_t hi = e + 1 >= 0 && e + 1 < V ? bf16_bits(z + e + 1) : 0xFF80u;
-            w[k] = lo | (hi << 16);
+      for (int j = 0; j < NV; ++j) {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r[j]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx = __hmax2(mx, h[k]);
+      }
+      // the warp's maximum is the reference of its threads: no rescaling before the sums are sent
+      wm = warp_max(fmaxf(__low2float(mx), __high2float(mx)));
+      const float ref = wm == -INFINITY ? 0.f : wm;
+      const f32x2 at2 = pair2(itl, itl), ct2 = pair2(-(ref * itl), -(ref * itl));
+      const f32x2 a12 = pair2(kLog2e, kLog2e), c12 = pair2(-(ref * kLog2e), -(ref * kLog2e));
+      f32x2 t0 = 0, t1 = 0, u0 = 0, u1 = 0;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          const f32x2 x0 = wide2(w[k]), x1 = wide2(w[k + 1]);
+          t0 = add2(t0, ex2_2(fma2(x0, at2, ct2)));
+          t1 = add2(t1, ex2_2(fma2(x1, at2, ct2)));
+          if (TWO) {
+            u0 = add2(u0, ex2_2(fma2(x0, a12, c12)));
+            u1 = add2(u1, ex2_2(fma2(x1, a12, c12)));
           }
-          r[j] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-    }
-    if (hard) zt = __bfloat162float(z[tgt]);
-    // packed maxima: exact, and NaN passes by (it shows in the sums)
-    __nv_bfloat162 mx = __halves2bfloat162(__ushort_as_bfloat16(0xFF80), __ushort_as_bfloat16(0xFF80));
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r[j]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) mx = __hmax2(mx, h[k]);
-    }
-    const float tm = fmaxf(__low2float(mx), __high2float(mx));
-    const float ref = tm == -INFINITY ? 0.f : tm;
-    float s1 = 0.f, st = 0.f;
-    if (two) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        float f[8];
-        unpack8(r[j], f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float x = f[k] - ref;
-          s1 += ex2(x * kLog2e);
-          st += ex2(x * itl);
-        }
-      }
+      const float2 t = unpair2(add2(t0, t1)), u = unpair2(add2(u0, u1));
+      st = warp_sum(t.x + t.y);
+      s1 = TWO ? warp_sum(u.x + u.y) : st;
     } else {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        float f[8];
-        unpack8(r[j], f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) st += ex2((f[k] - ref) * itl);
+      const bf16* z = a.logits + row * V;
+      const int tgt = tgt_next >= 0 && tgt_next < V ? tgt_next : -1;
+      float zt = 0.f;
+      if (tgt >= 0) zt = __bfloat162float(z[tgt]);
+      if (rank == 0) {
+        if (lane < head) ie = lane;
+        else if (lane >= 8 && head + nvec * 8 + lane - 8 < V) ie = head + nvec * 8 + lane - 8;
+        if (ie >= 0) ze = __bfloat162float(z[ie]);
       }
-      s1 = st;
+      // the teacher's slots; every block of the cluster needs them for its own columns
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      for (int j = lane; j < 2 * a.kcap; j += 32) table[j] = -1;
+      __syncwarp();
+      float ym = -INFINITY;
+      bool nan = false, twice = false, listed = false;
+#pragma unroll 4
+      for (int j = lane; j < K; j += 32) {
+        int i = id[j];
+        if (i < 0 || i >= V) i = -1;
+        zj[j] = i >= 0 ? __bfloat162float(z[i]) : 0.f;
+        const float v = i >= 0 ? y[j] * it : -INFINITY;
+        id[j] = i;
+        y[j] = v;
+        ym = fmaxf(ym, v);
+        nan |= v != v;
+        listed |= i >= 0 && i == tgt;
+      }
+      for (int j = lane; j < K; j += 32) {
+        const int i = id[j];
+        if (i < 0) continue;
+        uint32_t h = (uint32_t)i * 2654435761u >> 7;
+        for (;;) {  // ends: the table has twice as many places as there are slots
+          h &= 2u * (uint32_t)a.kcap - 1u;
+          const int old = atomicCAS(&table[h], -1, i);
+          if (old == i) twice = true;
+          if (old == -1 || old == i) break;
+          ++h;
+        }
+      }
+      ym = warp_max(ym);
+      nan = __any_sync(0xffffffffu, nan);
+      twice = __any_sync(0xffffffffu, twice);
+      listed = __any_sync(0xffffffffu, listed);
+      if (nan && ym == -INFINITY) ym = 0.f;  // a NaN among the slots shows in the row, it does not empty it
+      const bool some = ym != -INFINITY;
+      if (lane == 0) {
+        s_tgt[par] = tgt;
+        s_zt[par] = zt;
+        s_flags[par] = (some ? 1 : 0) | (twice ? 2 : 0) | (listed ? 4 : 0);
+      }
+      // the end elements' sums
+      wm = warp_max(ze);
+      const float ref = wm == -INFINITY ? 0.f : wm;
+      st = warp_sum(ie >= 0 ? ex2(fmaf(ze, itl, -(ref * itl))) : 0.f);
+      s1 = TWO ? warp_sum(ie >= 0 ? ex2(fmaf(ze, kLog2e, -(ref * kLog2e))) : 0.f) : st;
+      // the next row, once every warp has taken this one out of the buffer (and so has left the row before it,
+      // whose slots the next one's take the place of)
+      if (row + stride < a.rows) {
+        if (lane == 0) mbar_wait(&empty, (uint32_t)par, failed);
+        __syncwarp();
+        fetch(row + stride, par ^ 1);
+        place(row);
+      }
+      // q, up to the factor 1 / ysum
+      for (int j = lane; j < K; j += 32) {
+        const float d = y[j] - ym, v = id[j] < 0 || !some ? 0.f : expf(d);
+        y[j] = d;
+        q[j] = v;
+        ysum += v;
+      }
+      ysum = warp_sum(ysum);
     }
-    const float wm = warp_max(tm);
-    const float w1 = wm == -INFINITY ? 1.f : ex2((tm - wm) * kLog2e), wt = wm == -INFINITY ? 1.f : ex2((tm - wm) * itl);
-    s1 = warp_sum(s1 * w1);
-    st = warp_sum(st * wt);
     if (lane < (int)ncta) {
-      const uint32_t to = cluster_addr(&peer[rank * DW + warp][0], (uint32_t)lane);
+      const uint32_t to = cluster_addr(&peer[par][rank * (DW + 1) + warp][0], (uint32_t)lane);
       st_cluster(to, wm);
       st_cluster(to + 4, s1);
       st_cluster(to + 8, st);
     }
-  } else {
-    // the teacher's distribution; every block of the cluster needs it for its own columns
-    if (hard) zt = __bfloat162float(z[tgt]);
-    float ym = -INFINITY;
-    bool nan = false;
-#pragma unroll 4
-    for (int j = lane; j < K4; j += 32) {
-      const int i = j < K ? a.t_idx[row * K + j] : -1;
-      const bool in = i >= 0 && i < V;
-      const float v = in ? a.t_val[row * K + j] * it : -INFINITY;
-      id[j] = in ? i : -1;
-      y[j] = v;
-      zj[j] = in ? __bfloat162float(z[i]) : 0.f;
-      ym = fmaxf(ym, v);
-      nan |= v != v;
-    }
-    ym = warp_max(ym);
-    nan = __any_sync(0xffffffffu, nan);
-    if (nan && ym == -INFINITY) ym = 0.f;  // a NaN among the slots shows in the row, it does not empty it
-    __syncwarp();
-    const bool some = ym != -INFINITY;
-    float ys = 0.f;
-    for (int j = lane; j < K4; j += 32) {
-      const float d = y[j] - ym, v = id[j] < 0 || !some ? 0.f : expf(d);
-      y[j] = d;
-      q[j] = v;
-      ys += v;
-    }
-    ys = warp_sum(ys);
-    __syncwarp();
-    if (some)
-      for (int j = lane; j < K4; j += 32) q[j] = id[j] < 0 ? 0.f : q[j] / ys;
-    if (lane == 0) t_sum = some ? ys : 0.f;
-  }
-  cluster_sync();  // also: every read of the row by this cluster is done before its first write (in place)
+    cluster_sync();  // also: every read of the row by this cluster is done before its first write (in place)
 
-  const int np = (int)ncta * DW;
-  float m = -INFINITY;
-  for (int i = lane; i < np; i += 32) m = fmaxf(m, peer[i][0]);
-  m = warp_max(m);
-  float s1 = 0.f, st = 0.f;
-  for (int i = lane; i < np; i += 32) {
-    const float d = peer[i][0] - m;
-    s1 += peer[i][1] * (m == -INFINITY ? 1.f : ex2(d * kLog2e));
-    st += peer[i][2] * (m == -INFINITY ? 1.f : ex2(d * itl));
-  }
-  s1 = warp_sum(s1);
-  st = warp_sum(st);
-  const float ysum = t_sum;
-  const bool soft = !(ysum == 0.f);
-  // log p = (z - m) / tau - log S: differences first, so that the size of the logits costs no digits
-  const float l1 = logf(s1), lt = logf(st);
-  bf16* d = a.dlogits + row * V;
-  const float a1 = hard ? a.w_ce : 0.f, at = soft ? a.w_kd * it : 0.f;
-  if (warp == DW) {
-    if (rank == 0) {
+    const int np = (int)ncta * (DW + 1);
+    float m = -INFINITY;
+    for (int i = lane; i < np; i += 32) m = fmaxf(m, peer[par][i][0]);
+    m = warp_max(m);
+    if (m == -INFINITY) m = 0.f;
+    const float c1 = __fmul_rn(m, kLog2e), ct = __fmul_rn(m, itl);
+    s1 = st = 0.f;
+    for (int i = lane; i < np; i += 32) {
+      const float p = peer[par][i][0];
+      const bool none = p == -INFINITY;  // its sums are 0 (or NaN)
+      s1 += peer[par][i][1] * (none ? 1.f : ex2(__fmul_rn(p, kLog2e) - c1));
+      st += peer[par][i][2] * (none ? 1.f : ex2(__fmul_rn(p, itl) - ct));
+    }
+    s1 = warp_sum(s1);
+    st = warp_sum(st);
+    const int tgt = s_tgt[par], flags = s_flags[par];
+    const bool hard = tgt >= 0, soft = flags & 1;
+    bf16* d = a.dlogits + row * V;
+    const float w1 = hard ? a.w_ce : 0.f, wt = soft ? a.w_kd * it : 0.f;
+    const float f1 = hard ? w1 / s1 : 0.f, ft = soft ? wt / st : 0.f, fs = TWO ? ft : f1 + ft;
+    const float l1 = log2f(s1), lt = log2f(st);
+    if (warp == DW) {
       float kd = 0.f;
       const float yl = logf(ysum);
-      for (int j = lane; j < K; j += 32)
-        if (id[j] >= 0 && q[j] != 0.f) kd += q[j] * ((y[j] - yl) - ((zj[j] - m) * it - lt));
-      kd = warp_sum(kd);
-      if (lane == 0) {
-        a.row_kd[row] = soft ? kd : 0.f;
-        if (a.row_ce) a.row_ce[row] = hard ? l1 - (zt - m) : 0.f;
+      for (int j = lane; j < K; j += 32) {
+        if (id[j] < 0 || q[j] == 0.f) continue;
+        q[j] /= ysum;
+        kd += q[j] * ((y[j] - yl) - kLn2 * (fmaf(zj[j], itl, -ct) - lt));
       }
-    }
-  } else if (a.dlogits) {
-    uint4* dv = reinterpret_cast<uint4*>(d - skip);
-    const float c1 = hard ? a1 / s1 : 0.f, ct = soft ? at / st : 0.f, cs = two ? ct : c1 + ct;
-    const bool any = hard || soft;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int v = v0 + j * DT + tid, c = v * 8 - skip;
-      if (v >= v1) continue;
-      float f[8];
-      unpack8(r[j], f);
-      if (two) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float x = f[k] - m;
-          f[k] = c1 * ex2(x * kLog2e) + cs * ex2(x * itl);
+      if (rank == 0) {
+        kd = warp_sum(kd);
+        if (lane == 0) {
+          a.row_kd[row] = soft ? kd : 0.f;
+          if (a.row_ce) a.row_ce[row] = hard ? kLn2 * (l1 - fmaf(s_zt[par], kLog2e, -c1)) : 0.f;
         }
-      } else if (any) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = cs * ex2((f[k] - m) * itl);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = 0.f;
+        if (a.dlogits && ie >= 0) {
+          float v = soft || !TWO ? fs * ex2(fmaf(ze, itl, -ct)) : 0.f;
+          if (TWO && hard) v += f1 * ex2(fmaf(ze, kLog2e, -c1));
+          d[ie] = __float2bfloat16_rn(hard || soft ? v : 0.f);
+        }
       }
-      if (c >= 0 && c + 8 <= V) {
-        dv[v] = pack8(f);
-      } else {
+    } else if (a.dlogits) {
+      uint4* dv = reinterpret_cast<uint4*>(d + head);
+      const f32x2 at2 = pair2(itl, itl), ct2 = pair2(-ct, -ct), ft2 = pair2(fs, fs);
+      const f32x2 a12 = pair2(kLog2e, kLog2e), c12 = pair2(-c1, -c1), f12 = pair2(f1, f1);
+      if (hard || soft) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (c + k >= 0 && c + k < V) d[c + k] = __float2bfloat16_rn(f[k]);
+        for (int j = 0; j < NV; ++j) {
+          const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const f32x2 x = wide2(w[k]);
+            f32x2 v = mul2(ex2_2(fma2(x, at2, ct2)), ft2);
+            if (TWO) v = fma2(ex2_2(fma2(x, a12, c12)), f12, v);
+            const float2 t = unpair2(v);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(t.x, t.y);
+            o[k] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          if (v0 + j * DT < v1) dv[v0 + j * DT] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      } else {
+        for (int v = v0; v < v1; v += DT) dv[v] = make_uint4(0, 0, 0, 0);
       }
     }
-  }
-  if (!a.dlogits) return;
-  __syncthreads();  // the dense part of this block's columns is written
-  const int e0 = v0 * 8 - skip, e1 = v1 * 8 - skip;
-  for (int j = tid; j <= K; j += NT) {  // slot K: the target, if no slot names it
-    const int i = j < K ? id[j] : (hard ? tgt : -1);
-    if (i < 0 || i < e0 || i >= e1) continue;
-    bool first = true;
-    float qs = 0.f;
-    for (int u = 0; u < K4; u += 4) {
-      const int4 w = *reinterpret_cast<const int4*>(id + u);
-      if (w.x != i && w.y != i && w.z != i && w.w != i) continue;
-#pragma unroll 1
-      for (int k = u; k < u + 4; ++k) {
-        if (id[k] != i) continue;
-        if (k < j) first = false;
-        qs += q[k];
+    if (!a.dlogits) continue;
+    __syncthreads();  // the dense part of this block's columns is written, q is final
+    const int e0 = head + (int)rank * per * 8, e1 = head + v1 * 8;
+    for (int j = tid; j <= K; j += NT) {  // slot K: the target, if no slot names it
+      const int i = j < K ? id[j] : (flags & 4 ? -1 : tgt);
+      if (i < 0 || !((i >= e0 && i < e1) || (rank == 0 && (i < head || i >= head + nvec * 8)))) continue;
+      bool first = true;
+      float qs = j < K ? q[j] : 0.f;
+      if (flags & 2) {
+        qs = 0.f;
+        for (int u = 0; u < K; ++u) {
+          if (id[u] != i) continue;
+          if (u < j) first = false;
+          qs += q[u];
+        }
       }
+      if (!first) continue;
+      const float x = j < K ? zj[j] : s_zt[par];
+      float v = 0.f;
+      if (hard) {
+        const float lp = kLn2 * (fmaf(x, kLog2e, -c1) - l1);
+        v += w1 * (i == tgt ? expm1f(lp) : expf(lp));
+      }
+      if (soft) v += wt * (ex2(fmaf(x, itl, -ct) - lt) - qs);
+      d[i] = __float2bfloat16_rn(v);
     }
-    if (!first) continue;
-    const float x = (j < K ? zj[j] : zt) - m;
-    float v = 0.f;
-    if (hard) v += a1 * (i == tgt ? expm1f(x - l1) : expf(x - l1));
-    if (soft) v += at * (expf(x * it - lt) - qs);
-    d[i] = __float2bfloat16_rn(v);
   }
 }
 
@@ -628,7 +795,7 @@ __global__ void __launch_bounds__(BAL_THREADS, NV == 1 ? 2 : 1) balance_grad_k(c
     float e8[NV * 8];
 #pragma unroll
     for (int i = 0; i < NV * 8; ++i) {
-      e8[i] = x[i] == -INFINITY && m != -INFINITY ? 0.f : expf(x[i] - m);
+      e8[i] = ex2((x[i] - m) * kLog2e);  // 0 beyond E, where x is -inf
       s += e8[i];
     }
     const bool pad_lanes = !now;  // rows outside the block or padded: nothing below counts
@@ -670,8 +837,7 @@ __global__ void __launch_bounds__(BAL_THREADS, NV == 1 ? 2 : 1) balance_grad_k(c
     if (!pad_lanes) {
 #pragma unroll
       for (int i = 0; i < NV * 8; ++i) {
-        const int e = ((i >> 3) * LPR + sub) * 8 + (i & 7);
-        const float p = e < E ? e8[i] * is : 0.f;
+        const float p = e8[i] * is;
         P[i] += p;
         e8[i] = p * (cb * f[i] + shift);
       }
@@ -831,7 +997,7 @@ size_t ce_carve(int64_t T, int H, int V, bool grads, bool dW, uint8_t* base, CeS
     return p;
   };
   w->chunk = ce_chunk(T, V);
-  w->npieces = (V + 255) / 256;
+  w->npieces = (V + 127) / 128;
   w->ldE = up(V, 64);
   w->ctr = (int*)take(256);
   w->stat = (float2*)take(w->chunk * w->npieces * 8);
@@ -918,10 +1084,75 @@ cudaError_t launch_balance_grad(const BalArgs& a, cudaStream_t s) {
                       : launch(balance_grad_k<LPR, NV, false>, grid, BAL_THREADS, 0, 0, true, s, a);
 }
 
+// The join and the sum of runs stand between two GEMMs that use nearly all
+// shared memory: they ask for the same split of it and the L1 cache, which an
+// SM changes only when it is empty.  Set once per device.
+cudaError_t share_memory_config() {
+  constexpr int DEV = 16;
+  static std::atomic<int> done[DEV];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < DEV && done[dev].load(std::memory_order_acquire))) return e;
+  e = cudaFuncSetAttribute(ce_join_k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(ce_add_runs_k, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && dev < DEV) done[dev].store(1, std::memory_order_release);
+  return e;
+}
+
+// Clusters of a distillation kernel that are resident at once, looked up once
+// per device, form, cluster size and slot room.
+template <int NV, int NT, bool TWO>
+cudaError_t distill_resident(int cluster, int kcap, int* out) {
+  constexpr int DEV = 16;
+  static std::atomic<int> known[DEV][4][6];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int ci = 0, ki = 0;
+  while ((1 << ci) < cluster) ++ci;
+  while ((32 << ki) < kcap) ++ki;
+  std::atomic<int>* slot = dev < DEV ? &known[dev][ci][ki] : nullptr;
+  if (slot && (*out = slot->load(std::memory_order_acquire)) > 0) return cudaSuccess;
+  const size_t smem = kd_smem<NV, NT>(kcap);
+  // room for the most slots, so that the setting never shrinks under another call
+  e = cudaFuncSetAttribute(distill_k<NV, NT, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)kd_smem<NV, NT>(KD_MAX_K));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(cluster * 1024));
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, distill_k<NV, NT, TWO>, &cfg);
+  if (e != cudaSuccess) return e;
+  if (n < 1) return cudaErrorInvalidConfiguration;
+  if (slot) slot->store(n, std::memory_order_release);
+  *out = n;
+  return cudaSuccess;
+}
+
+template <int NV, int NT, bool TWO>
+cudaError_t launch_distill2(const KdArgs& a, int cluster, cudaStream_t s) {
+  int n = 0;
+  const cudaError_t e = distill_resident<NV, NT, TWO>(cluster, a.kcap, &n);
+  if (e != cudaSuccess) return e;
+  if (n > a.rows) n = (int)a.rows;
+  return launch(distill_k<NV, NT, TWO>, dim3((unsigned)(n * cluster)), NT, kd_smem<NV, NT>(a.kcap), cluster, false, s,
+                a);
+}
 template <int NV, int NT = 256>
-cudaError_t launch_distill(const KdArgs& a, int64_t rows, int cluster, cudaStream_t s) {
-  return launch(distill_k<NV, NT>, dim3((unsigned)(rows * cluster)), NT, (size_t)((a.K + 3) & ~3) * 16, cluster, false,
-                s, a);
+cudaError_t launch_distill(const KdArgs& a, int cluster, cudaStream_t s) {
+  return a.target && a.tau != 1.f ? launch_distill2<NV, NT, true>(a, cluster, s)
+                                  : launch_distill2<NV, NT, false>(a, cluster, s);
 }
 
 }  // namespace
@@ -943,19 +1174,24 @@ cudaError_t linear_cross_entropy(const bf16* h, const bf16* W, const int32_t* ta
   CeScratch w;
   if (ce_carve(T, H, V, grads, dW != nullptr, (uint8_t*)scratch, &w) > scratch_bytes) return cudaErrorInvalidValue;
   if (T == 0) return cudaSuccess;
-  cudaError_t e = cudaMemsetAsync(w.ctr, 0, 256, s);
-  if (e != cudaSuccess) return e;
+  // tiles are drawn from a counter where some pair takes more than one
+  const int64_t nt = (w.chunk + 255) / 256, nv = (V + 255) / 256, nh = (H + 255) / 256;
+  const bool draw = nt * nv > 76 || nh * (nt * w.runs + nv) > 76;
+  cudaError_t e = cudaSuccess;
+  if (draw && (e = cudaMemsetAsync(w.ctr, 0, 256, s)) != cudaSuccess) return e;
+  int* ctr = draw ? w.ctr : nullptr;
+  if ((e = share_memory_config()) != cudaSuccess) return e;
   for (int64_t c0 = 0; c0 < T; c0 += w.chunk) {
     const int rows = (int)(T - c0 < w.chunk ? T - c0 : w.chunk);
     const bool first = c0 == 0, last = c0 + rows >= T;
     const SoftmaxPieces sp{w.stat, w.npieces, target + c0, w.zt, w.E, w.ldE};
-    e = gemm_softmax_pieces(h + c0 * H, W, rows, V, H, sp, w.ctr, s);
+    e = gemm_softmax_pieces(h + c0 * H, W, rows, V, H, sp, ctr, !first, s);
     if (e != cudaSuccess) return e;
     // few rows: several blocks share each, down to about 2048 columns a block
     const int want = 1216 / rows, most = (V + 2047) / 2048, split = want < 1 || !w.E ? 1 : want < most ? want : most;
-    ce_join_k<<<dim3((unsigned)rows, (unsigned)split), JOIN_THREADS, 0, s>>>(w.stat, w.npieces, target + c0, w.zt, V,
-                                                                             row_loss + c0, w.E, w.ldE);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch(ce_join_k, dim3((unsigned)rows, (unsigned)split), JOIN_THREADS, 0, 0, true, s, (const float2*)w.stat,
+               w.npieces, target + c0, (const float*)w.zt, V, row_loss + c0, w.E, w.ldE);
+    if (e != cudaSuccess) return e;
     if (!grads) continue;
     const bf16* d = reinterpret_cast<const bf16*>(w.E);
     const GemmArgs gd{d, w.ldE, 0, W, H, 1, rows, H, V, dh ? dh + c0 * H : nullptr, H, nullptr, 0, nullptr, 0, 0};
@@ -964,13 +1200,13 @@ cudaError_t linear_cross_entropy(const bf16* h, const bf16* W, const int32_t* ta
       gw.Dacc = w.dWacc;
       gw.acc_mode = first ? 1 : 2;
     }
-    e = gemm_grads(GradArgs{dh ? &gd : nullptr, dW ? &gw : nullptr, g, w.runs, w.slabs, w.ctr}, s);
+    e = gemm_grads(GradArgs{dh ? &gd : nullptr, dW ? &gw : nullptr, g, w.runs, w.slabs, ctr}, s);
     if (e != cudaSuccess) return e;
     if (dh && w.runs > 1) {
       const int64_t n4 = (int64_t)rows * H / 4;
-      ce_add_runs_k<<<(unsigned)((n4 + 255) / 256), 256, 0, s>>>(reinterpret_cast<const float4*>(w.slabs), n4, w.runs, g,
-                                                                reinterpret_cast<uint2*>(dh + c0 * H));
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      e = launch(ce_add_runs_k, dim3((unsigned)((n4 + 255) / 256)), 256, 0, 0, true, s,
+                 reinterpret_cast<const float4*>(w.slabs), n4, w.runs, g, reinterpret_cast<uint2*>(dh + c0 * H));
+      if (e != cudaSuccess) return e;
     }
   }
   return cudaSuccess;
@@ -982,31 +1218,31 @@ cudaError_t distill_topk(const bf16* logits, const int32_t* target, const float*
   if (rows < 0 || rows > 0x7fffffff || V < 1 || K < 1 || K > KD_MAX_K || !(tau > 0.f) || !(tau < INFINITY) || !(1.f / tau < INFINITY) || !al16(logits) ||
       !al16(dlogits))
     return cudaErrorInvalidValue;
-  // vectors a row touches at most: rows of an odd V start anywhere in one
-  const int nvec = V % 8 == 0 ? V / 8 : (V + 14) / 8;
-  if (V > KD_MAX_V || nvec > KD_MAX_V / 8) return cudaErrorInvalidValue;
+  if (V > KD_MAX_V) return cudaErrorInvalidValue;
   if (rows == 0) return cudaSuccess;
-  const KdArgs a{logits, target, t_val, t_idx, V, K, tau, w_ce, w_kd, row_ce, row_kd, dlogits};
+  int kcap = 32;
+  while (kcap < K) kcap *= 2;
+  const KdArgs a{rows, kcap, logits, target, t_val, t_idx, V, K, tau, w_ce, w_kd, row_ce, row_kd, dlogits};
+  const int nvec = V / 8;  // whole vectors of a row at most
   // blocks of a cluster so that a thread holds up to 9 vectors (more at the
   // widest rows, where the cluster is at its largest)
   int cluster = 1;
   while (cluster < KD_MAX_CLUSTER && (nvec + cluster - 1) / cluster > 9 * 224) cluster *= 2;
-  if (rows * cluster > 0x7fffffff) return cudaErrorInvalidValue;
   const int per = (nvec + cluster - 1) / cluster;
   switch ((per + 223) / 224) {
-    case 1: return launch_distill<1>(a, rows, cluster, s);
-    case 2: return launch_distill<2>(a, rows, cluster, s);
-    case 3: return launch_distill<3>(a, rows, cluster, s);
-    case 4: return launch_distill<4>(a, rows, cluster, s);
-    case 5: return launch_distill<5>(a, rows, cluster, s);
-    case 6: return launch_distill<6>(a, rows, cluster, s);
-    case 7: return launch_distill<7>(a, rows, cluster, s);
-    case 8: return launch_distill<8>(a, rows, cluster, s);
-    case 9: return launch_distill<9>(a, rows, cluster, s);
-    case 10: case 11: return launch_distill<11>(a, rows, cluster, s);
-    case 12: case 13: return launch_distill<13>(a, rows, cluster, s);
-    case 14: case 15: return launch_distill<15>(a, rows, cluster, s);
-    default: return launch_distill<KD_WIDE_NV, 512>(a, rows, cluster, s);
+    case 0: case 1: return launch_distill<1>(a, cluster, s);
+    case 2: return launch_distill<2>(a, cluster, s);
+    case 3: return launch_distill<3>(a, cluster, s);
+    case 4: return launch_distill<4>(a, cluster, s);
+    case 5: return launch_distill<5>(a, cluster, s);
+    case 6: return launch_distill<6>(a, cluster, s);
+    case 7: return launch_distill<7>(a, cluster, s);
+    case 8: return launch_distill<8>(a, cluster, s);
+    case 9: return launch_distill<9>(a, cluster, s);
+    case 10: case 11: return launch_distill<11>(a, cluster, s);
+    case 12: case 13: return launch_distill<13>(a, cluster, s);
+    case 14: case 15: return launch_distill<15>(a, cluster, s);
+    default: return launch_distill<KD_WIDE_NV, 512>(a, cluster, s);
   }
 }
 
@@ -1044,6 +1280,15 @@ cudaError_t router_balance(const float* logits, const int32_t* idx, const uint8_
   if (E <= 128) return launch_balance_grad<16, 1>(a, s);
   if (E <= 256) return launch_balance_grad<32, 1>(a, s);
   return launch_balance_grad<32, 2>(a, s);
+}
+
+cudaError_t loss_error_read(int* code, int clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(code, g_loss_error, sizeof(int));
+  if (e == cudaSuccess && clear) {
+    const int z = 0;
+    e = cudaMemcpyToSymbol(g_loss_error, &z, sizeof(int));
+  }
+  return e;
 }
 
 }  // namespace mt

@@ -61,7 +61,7 @@ struct GemmKGroupArgs {
 };
 cudaError_t gemm_expert_kgroups(const GemmKGroupArgs& g, cudaStream_t s);
 // Softmax statistics of logits Z = A B^T ([M][N], K-major operands with row
-// stride K) that are never written: per row and piece of 256 columns, (m, s) =
+// stride K) that are never written: per row and piece of 128 columns, (m, s) =
 // (largest logit, sum exp(z - m) without the target's column) from the FP32
 // accumulators; with E, also E[m, n] = fp16_rne(2^15 exp(z - m of its piece)),
 // 0 at the target; zt[r] = the logit of column target[r] (rows whose target is
@@ -69,20 +69,23 @@ cudaError_t gemm_expert_kgroups(const GemmKGroupArgs& g, cudaStream_t s);
 // aligned, ldE a multiple of 8.
 struct SoftmaxPieces {
   float2* stat;           // [M][npieces]
-  int npieces;            // ceil(N / 256)
+  int npieces;            // ceil(N / 128)
   const int32_t* target;  // [M]
   float* zt;              // [M]
   uint16_t* E; int64_t ldE;  // null: statistics only
 };
-// tile_ctr: the launch's tile counter, zero on entry and left zero; the caller's
-// memory, so that launches of different callers share nothing.
+// tile_ctr: the launch's tile counter, zero on entry and left zero (null: every
+// n-th tile); the caller's memory, so that launches of different callers share
+// nothing.  dependent: the launch may begin while the kernel before it ends; it
+// waits for that kernel before it reads or writes.
 cudaError_t gemm_softmax_pieces(const bf16* A, const bf16* B, int M, int N, int K, const SoftmaxPieces& sp,
-                                int* tile_ctr, cudaStream_t s);
+                                int* tile_ctr, bool dependent, cudaStream_t s);
 // alpha dY W (a_mn = 0, b_mn = 1) and alpha dY^T X (a_mn = b_mn = 1), one of
 // them or both in one launch, the input gradient's tiles (the long sums of an
 // LM head) first.  alpha applies to D, not to Dacc.  ksplit > 1: the input
 // gradient's sum is cut into ksplit equal runs of K blocks (none may be empty)
-// whose FP32 products go to slabs [ksplit][M][N]; the caller adds them.
+// whose FP32 products go to slabs [ksplit][M][N]; the caller adds them.  The
+// launch is dependent on the one before it, as above.
 struct GradArgs {
   const GemmArgs *dgrad, *wgrad;
   float alpha;
@@ -103,10 +106,11 @@ int gemm_mode(int mode);
 int gemm_stall_take();
 
 // Device-side error word written by kernels whose bounded waits expired
-// (0 = none; the GEMM's and the tensor-core attention's).  Read / cleared by
+// (0 = none; the GEMM's, the tensor-core attention's and the losses').  Read / cleared by
 // the host.
 cudaError_t kernel_error_read(int* code, int clear);
 cudaError_t attention_error_read(int* code, int clear);
+cudaError_t loss_error_read(int* code, int clear);
 
 // ---------------------------------------------------------------- elementwise
 // RMSNorm forward: y = x * rstd * gamma, rstd = (mean(x^2) + eps)^-1/2.

@@ -162,6 +162,11 @@ def _want(name, t, dtype, shape, dev):
         _refuse(f"{name}: want a contiguous {dtype} tensor of shape {shape} on CUDA device {dev}, got {got}")
 
 
+def _raw_stream(dev):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev)  # _stream() without building a Stream object (3 us)
+
+
 def _scratch(t, dev):
     """Bytes of a workspace; the library itself refuses one that is too small."""
     if t is None or not t.is_contiguous() or t.get_device() != dev:
@@ -189,7 +194,7 @@ def linear_cross_entropy(h, W, target, inv_norm, row_loss, dh, dW, scratch):
     if dW is not None:
         _want("dW", dW, bf, (V, H), dev)
     _chk(_L().mt_linear_cross_entropy(_p(h), _p(W), _p(target), T, H, V, inv_norm, _p(row_loss), _p(dh), _p(dW),
-                                      _p(scratch), _scratch(scratch, dev), _stream()))
+                                      _p(scratch), _scratch(scratch, dev), _raw_stream(dev)))
 
 
 def distill_topk(logits, target, t_val, t_idx, tau, w_ce, w_kd, row_ce, row_kd, dlogits):
@@ -209,7 +214,7 @@ def distill_topk(logits, target, t_val, t_idx, tau, w_ce, w_kd, row_ce, row_kd, 
     if dlogits is not None:
         _want("dlogits", dlogits, torch.bfloat16, (rows, V), dev)
     _chk(_L().mt_distill_topk(_p(logits), _p(target), _p(t_val), _p(t_idx), rows, V, K, tau, w_ce, w_kd, _p(row_ce),
-                              _p(row_kd), _p(dlogits), _stream()))
+                              _p(row_kd), _p(dlogits), _raw_stream(dev)))
 
 
 def router_balance_scratch_bytes(T, S, E) -> int:
@@ -235,7 +240,7 @@ def router_balance(logits, idx, valid, S, alpha, z_coef, loss, counts, prob, dlo
     if dlogits is not None:
         _want("dlogits", dlogits, torch.bfloat16, (T, E), dev)
     _chk(_L().mt_router_balance(_p(logits), _p(idx), _p(valid), T, S, E, k, alpha, z_coef, _p(loss), _p(counts),
-                                _p(prob), _p(dlogits), _p(scratch), _scratch(scratch, dev), _stream()))
+                                _p(prob), _p(dlogits), _p(scratch), _scratch(scratch, dev), _raw_stream(dev)))
 
 
 def moe_scratch_bytes(T, H, E, k, Fe):

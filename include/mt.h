@@ -452,7 +452,7 @@ mt_status mt_cross_entropy(void* logits, const int32_t* target, int64_t rows, in
  * gradients dh ([T][H] BF16) and dW ([V][H] BF16, every row written); dh, dW
  * or both may be null and are then not computed.  A target outside [0, V)
  * marks a row with no target (zero loss, no gradient).  The softmax is taken
- * in pieces of 256 columns as the product's tiles come out; for the gradients
+ * in pieces of 128 columns as the product's tiles come out; for the gradients
  * the exponentials of a bounded chunk of tokens (up to 3 GiB) are held in 16
  * bits, relative to each piece's maximum, so their error does not grow with
  * the logits; over several chunks dW is summed in FP32.  scratch: 256-byte
@@ -477,9 +477,8 @@ mt_status mt_linear_cross_entropy(const void* h, const void* W, const int32_t* t
  * only; may be logits itself).  An id in several slots counts with the sum of
  * its q.  A row with no filled slot (or none above -inf) has no teacher part,
  * a target outside [0, V) no hard part; a row with neither gets zeros.
- * row_ce may be null.  V <= 524288 (524281 where V is not a multiple of 8),
- * 1 <= K <= 1024, tau and 1 / tau finite and > 0, logits and dlogits 16-byte
- * aligned, else MT_ERR_ARG. */
+ * row_ce may be null.  V <= 524288, 1 <= K <= 1024, tau and 1 / tau
+ * finite and > 0, logits and dlogits 16-byte aligned, else MT_ERR_ARG. */
 mt_status mt_distill_topk(const void* logits, const int32_t* target, const float* t_val, const int32_t* t_idx,
                           int64_t rows, int32_t V, int32_t K, float tau, float w_ce, float w_kd, float* row_ce,
                           float* row_kd, void* dlogits, void* stream);

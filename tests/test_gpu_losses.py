@@ -265,7 +265,8 @@ def check_kd(z, tgt, y, ids, tau, w_ce, w_kd, got):
                                             (5, 1000, 50, 0.7, False), (9, 1023, 33, 3.0, True), (4, 4096, 1024, 2.0, True),
                                             (6, 32000, 32, 2.0, True), (3, 50257, 64, 1.5, True), (2, 152064, 128, 1.0, True),
                                             (2, 201089, 5, 1.3, False), (3, 2047, 16, 1.0, False), (2, 16385, 16, 1.1, True),
-                                            (2, 262145, 16, 1.1, True), (1, 524288, 16, 1.1, True)])
+                                            (2, 262145, 16, 1.1, True), (1, 524288, 16, 1.1, True), (9, 524287, 3, 1.0, True),
+                                            (20, 5, 2, 1.2, True), (17, 9, 4, 1.0, True), (9, 14341, 40, 1.0, True)])
 def test_distill(R, V, K, tau, hard):
     z, tgt, y, ids = kd_inputs(R, V, K, 30 + R, hard)
     check_kd(z, tgt, y, ids, tau, 0.4, 0.6 * tau, run_kd(z, tgt, y, ids, tau, 0.4, 0.6 * tau))
