@@ -209,26 +209,21 @@ __device__ __forceinline__ float ex2(float x) {
 //   q = softmax over the filled slots of y / tau, p = softmax(z / tau),
 //   kd = sum_j q_j (log q_j - log p_{i_j}),  ce = lse(z) - z_target,
 //   dz_v = w_ce (softmax(z)_v - [v = target]) + w_kd / tau (p_v - sum_{i_j = v} q_j).
-// Bound by HBM: the row has to be known before its first gradient element, so
-// it is read once and kept: a cluster of 1 to 8 blocks holds a row in
-// registers, NV 16-byte vectors a thread.  The clusters are resident and take
-// every n-th row; a bulk copy brings a block's part of its next row to shared
-// memory while this one is worked on, so that no thread waits for HBM.  Every
-// warp sums exp(z - m) around its own maximum m at both temperatures and sends
-// (m, s1, st) to every block of the cluster through distributed shared memory;
-// after the one barrier a row has every warp joins them all, and the gradient
-// is computed from the same registers.  The last warp of a block holds no part
-// of the row: it issues the copies, and works out the teacher's distribution,
-// whose dependent loads would otherwise stand before the barrier.  The at most
-// K + 1 columns with a teacher entry or the target are written again from their
-// FP32 values by the block that holds them, each by one thread, so that no
-// element is rounded twice and an id that appears in several slots gets the sum
-// of their q, in slot order.
+// Bound by HBM: the statistics need the whole row before the first gradient
+// element.  A block takes one row at a time, and every n-th row: a producer
+// lane streams the row through a ring of shared memory with bulk copies, always
+// ahead of the warps that work on it, across row ends.  Where a row fits the
+// ring it stays there until its gradient is written; a longer one is fetched a
+// second time, from L2 (152 rows under work are at most 46 MB of 152064
+// columns).  The working warps take running sums of exp(z - m) around each
+// thread's maximum m at both temperatures, join them once per row, and write
+// the dense part of the gradient.  A further warp works out the teacher's
+// distribution of the next row meanwhile, and rewrites the at most K + 1
+// columns with a teacher entry or the target from their FP32 values once the
+// dense part stands, so that no element is rounded twice and an id that appears
+// in several slots gets the sum of their q, in slot order.
 constexpr int KD_MAX_K = 1024;
-constexpr int KD_MAX_CLUSTER = 8;
-constexpr int KD_WIDE_NV = 18;
-constexpr int KD_MAX_V = 524288;
-static_assert(KD_MAX_CLUSTER * 480 * KD_WIDE_NV * 8 >= KD_MAX_V, "the widest form holds the widest row");
+constexpr int KD_U = 4;  // 16-byte vectors of a thread per chunk of the ring
 
 struct KdArgs {
   int64_t rows;
@@ -327,157 +322,124 @@ __device__ __forceinline__ void async_load4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(su32(dst)), "l"(src) : "memory");
 }
 
-// Blocks per SM that the registers are to allow: the row's 4 NV and about 36
-// more a thread, else the compiler keeps unpacked copies of the row (254 registers at NV = 12).
-template <int NV, int NT>
-constexpr int kd_blocks() {
-  return 65536 / (NT * (4 * NV + 36)) > 6 ? 6 : 65536 / (NT * (4 * NV + 36));
+template <int ID>
+__device__ __forceinline__ void named_sync(int n) {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "r"(n) : "memory");
 }
-template <int NV, int NT>
+template <int ID>
+__device__ __forceinline__ void named_arrive(int n) {
+  asm volatile("bar.arrive %0, %1;" ::"n"(ID), "r"(n) : "memory");
+}
+
+template <int CW, int NS>
 constexpr size_t kd_smem(int kcap) {
-  return (size_t)NV * (NT - 32) * 16 + (size_t)kcap * (2 * 4 + 2) * 4;
+  return (size_t)NS * CW * 32 * KD_U * 16 + (size_t)kcap * (2 * 4 + 2) * 4;
 }
-// TWO: both temperatures are summed (hard targets and tau != 1); else one
-// exponential serves both.  Exponentials are taken as 2^(z a - c) with a =
-// log2(e) or log2(e) / tau and the reference c = fl(m a) kept as it is rounded,
-// so that the fused product loses nothing.
-template <int NV, int NT, bool TWO>
-__global__ void __launch_bounds__(NT, kd_blocks<NV, NT>()) distill_k(const KdArgs a) {
-  constexpr int DT = NT - 32, DW = DT / 32;  // threads and warps that hold the row
+// CW working warps, a ring of NS chunks, BPS blocks per SM that the registers
+// are to allow.  TWO: both temperatures are summed (hard targets and tau != 1);
+// else one exponential serves both.  Exponentials are taken as 2^(z a - c) with
+// a = log2(e) or log2(e) / tau and the reference c = fl(m a) kept as it is
+// rounded, so that the fused product loses nothing.
+template <int CW, int NS, int BPS, bool TWO>
+__global__ void __launch_bounds__((CW + 2) * 32, BPS) distill_k(const KdArgs a) {
+  constexpr int CT = CW * 32, CV = CT * KD_U;  // threads that work on the row; vectors of a chunk
   extern __shared__ __align__(128) uint8_t smem[];
-  uint4* buf = reinterpret_cast<uint4*>(smem);                       // [NV][DT]: this block's part of the next row
-  float* slots = reinterpret_cast<float*>(smem + NV * DT * 16);      // two rows' slots, used in turn
-  int* table = reinterpret_cast<int*>(slots + 2 * 4 * a.kcap);       // [2 kcap] ids seen, -1 free
-  __shared__ float peer[2][KD_MAX_CLUSTER * (DW + 1)][3];
-  __shared__ int s_tgt[2];       // the row's target, -1: none
-  __shared__ float s_zt[2];      // its logit
-  __shared__ int s_flags[2];     // 1: a teacher, 2: an id in several slots, 4: the target in a slot
-  __shared__ uint64_t full, empty;
+  uint4* ring = reinterpret_cast<uint4*>(smem);                    // [NS][CV]
+  float* slots = reinterpret_cast<float*>(smem + NS * CV * 16);    // two rows' slots, used in turn
+  int* table = reinterpret_cast<int*>(slots + 2 * 4 * a.kcap);     // [2 kcap] ids seen, -1 free
+  __shared__ float part[2][CW + 1][3];  // (m, s1, st) of the warps; the last one's is of the row's ends
+  __shared__ int s_tgt[2];              // the row's target, -1: none
+  __shared__ int s_soft[2];             // whether it has a teacher
+  __shared__ uint64_t full[NS], empty[NS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int V = a.V, K = a.K;
-  const uint32_t rank = cluster_rank(), ncta = cluster_size();
-  const int64_t first_row = blockIdx.x / ncta, stride = gridDim.x / ncta;
   const float it = 1.f / a.tau, itl = it * kLog2e;
   constexpr float kLn2 = 0.6931471805599453f;
+  const bool grad = a.dlogits != nullptr;
   bool failed = false;
   if (tid == 0) {
-    mbar_init(&full, 1);
-    mbar_init(&empty, DW);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], CW);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  cluster_sync();  // the barriers are ready, and every block of the cluster has started
-
+  __syncthreads();
   // the row in memory: up to 7 elements, whole 16-byte vectors, up to 7
-  // elements.  The vectors are shared out to the blocks; the elements at the
-  // ends belong to lanes of block 0's last warp.
-  int head, nvec, per;
+  // elements.  The vectors go through the ring; the elements at the ends belong
+  // to lanes of the teacher's warp.
+  int head, nvec, nc;
+  bool held;  // the row stays in the ring until its gradient is written
   auto place = [&](int64_t row) {
     const int skip = (int)((row * V) & 7);
     head = skip ? min(8 - skip, V) : 0;
     nvec = (V - head) >> 3;
-    per = (nvec + (int)ncta - 1) / (int)ncta;
+    nc = (nvec + CV - 1) / CV;
+    held = grad && nc <= NS;
   };
-  int tgt_next = -1;
-  auto fetch = [&](int64_t row, int par) {  // the last warp: start everything row `row` needs on its way
-    place(row);
+
+  if (warp == CW + 1) {  // producer
     if (lane == 0) {
-      const int n = min(nvec, ((int)rank + 1) * per) - (int)rank * per;
-      if (n > 0) {
-        mbar_expect_tx(&full, (uint32_t)n * 16);
-        bulk_load(buf, a.logits + row * V + head + (int64_t)rank * per * 8, (uint32_t)n * 16, &full);
-      } else {
-        mbar_arrive(&full);
-      }
-    }
-    float* sl = slots + par * 4 * a.kcap;
-    for (int j = lane; j < K; j += 32) {
-      async_load4(sl + j, a.t_idx + row * K + j);
-      async_load4(sl + a.kcap + j, a.t_val + row * K + j);
-    }
-    tgt_next = a.target ? a.target[row] : -1;
-  };
-  if (warp == DW && first_row < a.rows) fetch(first_row, 0);
-
-  int turn = 0;
-  for (int64_t row = first_row; row < a.rows; row += stride, ++turn) {
-    const int par = turn & 1;
-    int* id = reinterpret_cast<int*>(slots + par * 4 * a.kcap);
-    float *y = reinterpret_cast<float*>(id) + a.kcap, *q = y + a.kcap, *zj = q + a.kcap;
-    place(row);
-    const int v0 = (int)rank * per + tid, v1 = min(nvec, ((int)rank + 1) * per);
-    uint4 r[NV];
-    float ze = -INFINITY;  // an end element
-    int ie = -1;           // its index
-    float wm, s1, st, ysum = 0.f;
-
-    if (warp < DW) {
-      mbar_wait(&full, (uint32_t)par, failed);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        r[j] = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);  // -inf: no probability
-        if (v0 + j * DT < v1) r[j] = buf[j * DT + tid];
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty);
-      // packed maxima: exact, and NaN passes by (it shows in the sums)
-      __nv_bfloat162 mx = __halves2bfloat162(__ushort_as_bfloat16(0xFF80), __ushort_as_bfloat16(0xFF80));
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r[j]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mx = __hmax2(mx, h[k]);
-      }
-      // the warp's maximum is the reference of its threads: no rescaling before the sums are sent
-      wm = warp_max(fmaxf(__low2float(mx), __high2float(mx)));
-      const float ref = wm == -INFINITY ? 0.f : wm;
-      const f32x2 at2 = pair2(itl, itl), ct2 = pair2(-(ref * itl), -(ref * itl));
-      const f32x2 a12 = pair2(kLog2e, kLog2e), c12 = pair2(-(ref * kLog2e), -(ref * kLog2e));
-      f32x2 t0 = 0, t1 = 0, u0 = 0, u1 = 0;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
-#pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-          const f32x2 x0 = wide2(w[k]), x1 = wide2(w[k + 1]);
-          t0 = add2(t0, ex2_2(fma2(x0, at2, ct2)));
-          t1 = add2(t1, ex2_2(fma2(x1, at2, ct2)));
-          if (TWO) {
-            u0 = add2(u0, ex2_2(fma2(x0, a12, c12)));
-            u1 = add2(u1, ex2_2(fma2(x1, a12, c12)));
+      int slot = 0;
+      uint32_t ph = 1;  // the ring starts empty
+      for (int64_t row = blockIdx.x; row < a.rows && !failed; row += gridDim.x) {
+        place(row);
+        const uint4* src = reinterpret_cast<const uint4*>(a.logits + row * V + head);
+        for (int pass = grad && !held ? 0 : 1; pass < 2 && !failed; ++pass)
+          for (int c = 0; c < nc; ++c) {
+            mbar_wait(&empty[slot], ph, failed);
+            if (failed) break;
+            const uint32_t bytes = (uint32_t)min(nvec - c * CV, CV) * 16;
+            mbar_expect_tx(&full[slot], bytes);
+            bulk_load(ring + slot * CV, src + (int64_t)c * CV, bytes, &full[slot]);
+            if (++slot == NS) {
+              slot = 0;
+              ph ^= 1;
+            }
           }
+      }
+      if (failed) {  // nothing more is issued; what is on its way lands before the block's memory goes
+        const long long t0 = clock64();
+        while (clock64() - t0 < kWaitCycles) {
         }
       }
-      const float2 t = unpair2(add2(t0, t1)), u = unpair2(add2(u0, u1));
-      st = warp_sum(t.x + t.y);
-      s1 = TWO ? warp_sum(u.x + u.y) : st;
-    } else {
+    }
+    return;
+  }
+
+  if (warp == CW) {  // the teacher
+    int turn = 0;
+    float zt = 0.f, ze = -INFINITY, ysum = 0.f;
+    int tgt = -1, ie = -1;
+    bool twice = false, listed = false, soft = false;
+    // everything of a row that its statistics do not enter; its slots' arrays are those of its turn
+    auto prepare = [&](int64_t row, int par) {
+      place(row);
       const bf16* z = a.logits + row * V;
-      const int tgt = tgt_next >= 0 && tgt_next < V ? tgt_next : -1;
-      float zt = 0.f;
-      if (tgt >= 0) zt = __bfloat162float(z[tgt]);
-      if (rank == 0) {
-        if (lane < head) ie = lane;
-        else if (lane >= 8 && head + nvec * 8 + lane - 8 < V) ie = head + nvec * 8 + lane - 8;
-        if (ie >= 0) ze = __bfloat162float(z[ie]);
-      }
-      // the teacher's slots; every block of the cluster needs them for its own columns
-      asm volatile("cp.async.wait_all;" ::: "memory");
+      int* id = reinterpret_cast<int*>(slots + par * 4 * a.kcap);
+      float *y = reinterpret_cast<float*>(id) + a.kcap, *q = y + a.kcap, *zj = q + a.kcap;
+      tgt = a.target ? a.target[row] : -1;
+      if (tgt >= V || tgt < 0) tgt = -1;
       for (int j = lane; j < 2 * a.kcap; j += 32) table[j] = -1;
-      __syncwarp();
+      ie = lane < head ? lane : lane >= 8 && head + nvec * 8 + lane - 8 < V ? head + nvec * 8 + lane - 8 : -1;
+      ze = ie >= 0 ? __bfloat162float(z[ie]) : -INFINITY;
       float ym = -INFINITY;
-      bool nan = false, twice = false, listed = false;
+      bool nan = false;
+      twice = listed = false;
 #pragma unroll 4
       for (int j = lane; j < K; j += 32) {
-        int i = id[j];
+        int i = a.t_idx[row * K + j];
         if (i < 0 || i >= V) i = -1;
+        const float v = i >= 0 ? a.t_val[row * K + j] * it : -INFINITY;
         zj[j] = i >= 0 ? __bfloat162float(z[i]) : 0.f;
-        const float v = i >= 0 ? y[j] * it : -INFINITY;
         id[j] = i;
         y[j] = v;
         ym = fmaxf(ym, v);
         nan |= v != v;
         listed |= i >= 0 && i == tgt;
       }
+      zt = tgt >= 0 ? __bfloat162float(z[tgt]) : 0.f;
+      __syncwarp();
       for (int j = lane; j < K; j += 32) {
         const int i = id[j];
         if (i < 0) continue;
@@ -495,64 +457,48 @@ __global__ void __launch_bounds__(NT, kd_blocks<NV, NT>()) distill_k(const KdArg
       twice = __any_sync(0xffffffffu, twice);
       listed = __any_sync(0xffffffffu, listed);
       if (nan && ym == -INFINITY) ym = 0.f;  // a NaN among the slots shows in the row, it does not empty it
-      const bool some = ym != -INFINITY;
-      if (lane == 0) {
-        s_tgt[par] = tgt;
-        s_zt[par] = zt;
-        s_flags[par] = (some ? 1 : 0) | (twice ? 2 : 0) | (listed ? 4 : 0);
-      }
-      // the end elements' sums
-      wm = warp_max(ze);
-      const float ref = wm == -INFINITY ? 0.f : wm;
-      st = warp_sum(ie >= 0 ? ex2(fmaf(ze, itl, -(ref * itl))) : 0.f);
-      s1 = TWO ? warp_sum(ie >= 0 ? ex2(fmaf(ze, kLog2e, -(ref * kLog2e))) : 0.f) : st;
-      // the next row, once every warp has taken this one out of the buffer (and so has left the row before it,
-      // whose slots the next one's take the place of)
-      if (row + stride < a.rows) {
-        if (lane == 0) mbar_wait(&empty, (uint32_t)par, failed);
-        __syncwarp();
-        fetch(row + stride, par ^ 1);
-        place(row);
-      }
-      // q, up to the factor 1 / ysum
+      soft = ym != -INFINITY;
+      ysum = 0.f;
       for (int j = lane; j < K; j += 32) {
-        const float d = y[j] - ym, v = id[j] < 0 || !some ? 0.f : expf(d);
+        const float d = y[j] - ym, v = id[j] < 0 || !soft ? 0.f : expf(d);
         y[j] = d;
         q[j] = v;
         ysum += v;
       }
       ysum = warp_sum(ysum);
-    }
-    if (lane < (int)ncta) {
-      const uint32_t to = cluster_addr(&peer[par][rank * (DW + 1) + warp][0], (uint32_t)lane);
-      st_cluster(to, wm);
-      st_cluster(to + 4, s1);
-      st_cluster(to + 8, st);
-    }
-    cluster_sync();  // also: every read of the row by this cluster is done before its first write (in place)
-
-    const int np = (int)ncta * (DW + 1);
-    float m = -INFINITY;
-    for (int i = lane; i < np; i += 32) m = fmaxf(m, peer[par][i][0]);
-    m = warp_max(m);
-    if (m == -INFINITY) m = 0.f;
-    const float c1 = __fmul_rn(m, kLog2e), ct = __fmul_rn(m, itl);
-    s1 = st = 0.f;
-    for (int i = lane; i < np; i += 32) {
-      const float p = peer[par][i][0];
-      const bool none = p == -INFINITY;  // its sums are 0 (or NaN)
-      s1 += peer[par][i][1] * (none ? 1.f : ex2(__fmul_rn(p, kLog2e) - c1));
-      st += peer[par][i][2] * (none ? 1.f : ex2(__fmul_rn(p, itl) - ct));
-    }
-    s1 = warp_sum(s1);
-    st = warp_sum(st);
-    const int tgt = s_tgt[par], flags = s_flags[par];
-    const bool hard = tgt >= 0, soft = flags & 1;
-    bf16* d = a.dlogits + row * V;
-    const float w1 = hard ? a.w_ce : 0.f, wt = soft ? a.w_kd * it : 0.f;
-    const float f1 = hard ? w1 / s1 : 0.f, ft = soft ? wt / st : 0.f, fs = TWO ? ft : f1 + ft;
-    const float l1 = log2f(s1), lt = log2f(st);
-    if (warp == DW) {
+      const float wm = warp_max(ze), ref = wm == -INFINITY ? 0.f : wm;
+      const float st = warp_sum(ie >= 0 ? ex2(fmaf(ze, itl, -__fmul_rn(ref, itl))) : 0.f);
+      const float s1 = TWO ? warp_sum(ie >= 0 ? ex2(fmaf(ze, kLog2e, -__fmul_rn(ref, kLog2e))) : 0.f) : st;
+      if (lane == 0) {
+        part[par][CW][0] = wm;
+        part[par][CW][1] = s1;
+        part[par][CW][2] = st;
+        s_tgt[par] = tgt;
+        s_soft[par] = soft;
+      }
+    };
+    if ((int64_t)blockIdx.x < a.rows) prepare(blockIdx.x, 0);
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++turn) {
+      const int par = turn & 1;
+      named_sync<1>(CT + 32);  // the row's statistics
+      float m = lane <= CW ? part[par][lane <= CW ? lane : 0][0] : -INFINITY;
+      const float pm = m;
+      m = warp_max(m);
+      if (m == -INFINITY) m = 0.f;
+      const float c1 = __fmul_rn(m, kLog2e), ct = __fmul_rn(m, itl);
+      float s1 = 0.f, st = 0.f;
+      if (lane <= CW) {
+        const bool none = pm == -INFINITY;
+        s1 = part[par][lane][1] * (none ? 1.f : ex2(__fmul_rn(pm, kLog2e) - c1));
+        st = part[par][lane][2] * (none ? 1.f : ex2(__fmul_rn(pm, itl) - ct));
+      }
+      s1 = warp_sum(s1);
+      st = warp_sum(st);
+      const bool hard = tgt >= 0;
+      const float l1 = log2f(s1), lt = log2f(st);
+      const float w1 = hard ? a.w_ce : 0.f, wt = soft ? a.w_kd * it : 0.f;
+      int* id = reinterpret_cast<int*>(slots + par * 4 * a.kcap);
+      float *y = reinterpret_cast<float*>(id) + a.kcap, *q = y + a.kcap, *zj = q + a.kcap;
       float kd = 0.f;
       const float yl = logf(ysum);
       for (int j = lane; j < K; j += 32) {
@@ -560,25 +506,171 @@ __global__ void __launch_bounds__(NT, kd_blocks<NV, NT>()) distill_k(const KdArg
         q[j] /= ysum;
         kd += q[j] * ((y[j] - yl) - kLn2 * (fmaf(zj[j], itl, -ct) - lt));
       }
-      if (rank == 0) {
-        kd = warp_sum(kd);
-        if (lane == 0) {
-          a.row_kd[row] = soft ? kd : 0.f;
-          if (a.row_ce) a.row_ce[row] = hard ? kLn2 * (l1 - fmaf(s_zt[par], kLog2e, -c1)) : 0.f;
+      kd = warp_sum(kd);
+      if (lane == 0) {
+        a.row_kd[row] = soft ? kd : 0.f;
+        if (a.row_ce) a.row_ce[row] = hard ? kLn2 * (l1 - fmaf(zt, kLog2e, -c1)) : 0.f;
+      }
+      const float zt0 = zt;
+      const int tgt0 = tgt;
+      const bool soft0 = soft, twice0 = twice, listed0 = listed;
+      if (grad && ie >= 0) {  // the row's ends
+        float v = 0.f;
+        if (hard) v += w1 / s1 * ex2(fmaf(ze, kLog2e, -c1));
+        if (soft) v += wt / st * ex2(fmaf(ze, itl, -ct));
+        a.dlogits[row * V + ie] = __float2bfloat16_rn(v);
+      }
+      if (row + gridDim.x < a.rows) prepare(row + gridDim.x, par ^ 1);
+      if (!grad) continue;
+      named_sync<2>(CT + 32);  // the dense part of the row is written
+      bf16* d = a.dlogits + row * V;
+      for (int j = lane; j <= K; j += 32) {  // slot K: the target, if no slot names it
+        const int i = j < K ? id[j] : (listed0 ? -1 : tgt0);
+        if (i < 0) continue;
+        bool first = true;
+        float qs = j < K ? q[j] : 0.f;
+        if (twice0) {
+          qs = 0.f;
+          for (int u = 0; u < K; ++u) {
+            if (id[u] != i) continue;
+            if (u < j) first = false;
+            qs += q[u];
+          }
         }
-        if (a.dlogits && ie >= 0) {
-          float v = soft || !TWO ? fs * ex2(fmaf(ze, itl, -ct)) : 0.f;
-          if (TWO && hard) v += f1 * ex2(fmaf(ze, kLog2e, -c1));
-          d[ie] = __float2bfloat16_rn(hard || soft ? v : 0.f);
+        if (!first) continue;
+        const float x = j < K ? zj[j] : zt0;
+        float v = 0.f;
+        if (hard) {
+          const float lp = kLn2 * (fmaf(x, kLog2e, -c1) - l1);
+          v += w1 * (i == tgt0 ? expm1f(lp) : expf(lp));
+        }
+        if (soft0) v += wt * (ex2(fmaf(x, itl, -ct) - lt) - qs);
+        d[i] = __float2bfloat16_rn(v);
+      }
+      __syncwarp();
+    }
+    return;
+  }
+
+  // the working warps
+  int slot = 0, turn = 0;
+  uint32_t ph = 0;
+  auto step = [&] {
+    if (++slot == NS) {
+      slot = 0;
+      ph ^= 1;
+    }
+  };
+  auto free_slot = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[slot]);
+  };
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++turn) {
+    const int par = turn & 1;
+    place(row);
+    const int slot0 = slot;
+    const uint32_t ph0 = ph;
+    float m = -INFINITY;
+    f32x2 t0 = 0, t1 = 0, u0 = 0, u1 = 0;
+    const f32x2 at2 = pair2(itl, itl), a12 = pair2(kLog2e, kLog2e);
+    for (int c = 0; c < nc; ++c) {
+      mbar_wait(&full[slot], ph, failed);
+      const uint4* b = ring + slot * CV;
+      uint4 r[KD_U];
+#pragma unroll
+      for (int j = 0; j < KD_U; ++j) {
+        r[j] = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);  // -inf: no probability
+        if (c * CV + j * CT + tid < nvec) r[j] = b[j * CT + tid];
+      }
+      if (!held) free_slot();
+      step();
+      // packed maxima: exact, and NaN passes by (it shows in the sums)
+      __nv_bfloat162 mx = __halves2bfloat162(__ushort_as_bfloat16(0xFF80), __ushort_as_bfloat16(0xFF80));
+#pragma unroll
+      for (int j = 0; j < KD_U; ++j) {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r[j]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx = __hmax2(mx, h[k]);
+      }
+      const float mc = fmaxf(__low2float(mx), __high2float(mx));
+      if (mc > m) {  // a new maximum: the sums so far move to it
+        if (m != -INFINITY) {
+          const float ft = ex2(__fmul_rn(m, itl) - __fmul_rn(mc, itl));
+          t0 = mul2(t0, pair2(ft, ft));
+          t1 = mul2(t1, pair2(ft, ft));
+          if (TWO) {
+            const float f1 = ex2(__fmul_rn(m, kLog2e) - __fmul_rn(mc, kLog2e));
+            u0 = mul2(u0, pair2(f1, f1));
+            u1 = mul2(u1, pair2(f1, f1));
+          }
+        }
+        m = mc;
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+      const float nct = -__fmul_rn(ref, itl), nc1 = -__fmul_rn(ref, kLog2e);
+      const f32x2 ct2 = pair2(nct, nct), c12 = pair2(nc1, nc1);
+#pragma unroll
+      for (int j = 0; j < KD_U; ++j) {
+        const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          const f32x2 x0 = wide2(w[k]), x1 = wide2(w[k + 1]);
+          t0 = add2(t0, ex2_2(fma2(x0, at2, ct2)));
+          t1 = add2(t1, ex2_2(fma2(x1, at2, ct2)));
+          if (TWO) {
+            u0 = add2(u0, ex2_2(fma2(x0, a12, c12)));
+            u1 = add2(u1, ex2_2(fma2(x1, a12, c12)));
+          }
         }
       }
-    } else if (a.dlogits) {
-      uint4* dv = reinterpret_cast<uint4*>(d + head);
-      const f32x2 at2 = pair2(itl, itl), ct2 = pair2(-ct, -ct), ft2 = pair2(fs, fs);
-      const f32x2 a12 = pair2(kLog2e, kLog2e), c12 = pair2(-c1, -c1), f12 = pair2(f1, f1);
+    }
+    {
+      const float2 t = unpair2(add2(t0, t1)), u = unpair2(add2(u0, u1));
+      const float wm = warp_max(m), M = wm == -INFINITY ? 0.f : wm;
+      const bool none = m == -INFINITY;  // its sums are 0 (or NaN)
+      const float st = warp_sum((t.x + t.y) * (none ? 1.f : ex2(__fmul_rn(m, itl) - __fmul_rn(M, itl))));
+      const float s1 = TWO ? warp_sum((u.x + u.y) * (none ? 1.f : ex2(__fmul_rn(m, kLog2e) - __fmul_rn(M, kLog2e)))) : st;
+      if (lane == 0) {
+        part[par][warp][0] = wm;
+        part[par][warp][1] = s1;
+        part[par][warp][2] = st;
+      }
+    }
+    named_sync<1>(CT + 32);
+    if (!grad) continue;
+    m = lane <= CW ? part[par][lane <= CW ? lane : 0][0] : -INFINITY;
+    const float pm = m;
+    m = warp_max(m);
+    if (m == -INFINITY) m = 0.f;
+    const float c1 = __fmul_rn(m, kLog2e), ct = __fmul_rn(m, itl);
+    float s1 = 0.f, st = 0.f;
+    if (lane <= CW) {
+      const bool none = pm == -INFINITY;
+      s1 = part[par][lane][1] * (none ? 1.f : ex2(__fmul_rn(pm, kLog2e) - c1));
+      st = part[par][lane][2] * (none ? 1.f : ex2(__fmul_rn(pm, itl) - ct));
+    }
+    s1 = warp_sum(s1);
+    st = warp_sum(st);
+    const bool hard = s_tgt[par] >= 0, soft = s_soft[par];
+    const float f1 = hard ? a.w_ce / s1 : 0.f, ft = soft ? a.w_kd * it / st : 0.f, fs = TWO ? ft : f1 + ft;
+    uint4* dv = reinterpret_cast<uint4*>(a.dlogits + row * V + head);
+    const f32x2 ct2 = pair2(-ct, -ct), ft2 = pair2(fs, fs), c12 = pair2(-c1, -c1), f12 = pair2(f1, f1);
+    if (held) {
+      slot = slot0;
+      ph = ph0;
+    }
+    for (int c = 0; c < nc; ++c) {
+      if (!held) mbar_wait(&full[slot], ph, failed);
+      const uint4* b = ring + slot * CV;
+      uint4 r[KD_U];
+#pragma unroll
+      for (int j = 0; j < KD_U; ++j)
+        if (c * CV + j * CT + tid < nvec) r[j] = b[j * CT + tid];
+      free_slot();
+      step();
       if (hard || soft) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
+        for (int j = 0; j < KD_U; ++j) {
           const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
           uint32_t o[4];
 #pragma unroll
@@ -590,38 +682,17 @@ __global__ void __launch_bounds__(NT, kd_blocks<NV, NT>()) distill_k(const KdArg
             const __nv_bfloat162 h = __floats2bfloat162_rn(t.x, t.y);
             o[k] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          if (v0 + j * DT < v1) dv[v0 + j * DT] = make_uint4(o[0], o[1], o[2], o[3]);
+          r[j] = make_uint4(o[0], o[1], o[2], o[3]);
         }
       } else {
-        for (int v = v0; v < v1; v += DT) dv[v] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < KD_U; ++j) r[j] = make_uint4(0, 0, 0, 0);
       }
+#pragma unroll
+      for (int j = 0; j < KD_U; ++j)
+        if (c * CV + j * CT + tid < nvec) dv[c * CV + j * CT + tid] = r[j];
     }
-    if (!a.dlogits) continue;
-    __syncthreads();  // the dense part of this block's columns is written, q is final
-    const int e0 = head + (int)rank * per * 8, e1 = head + v1 * 8;
-    for (int j = tid; j <= K; j += NT) {  // slot K: the target, if no slot names it
-      const int i = j < K ? id[j] : (flags & 4 ? -1 : tgt);
-      if (i < 0 || !((i >= e0 && i < e1) || (rank == 0 && (i < head || i >= head + nvec * 8)))) continue;
-      bool first = true;
-      float qs = j < K ? q[j] : 0.f;
-      if (flags & 2) {
-        qs = 0.f;
-        for (int u = 0; u < K; ++u) {
-          if (id[u] != i) continue;
-          if (u < j) first = false;
-          qs += q[u];
-        }
-      }
-      if (!first) continue;
-      const float x = j < K ? zj[j] : s_zt[par];
-      float v = 0.f;
-      if (hard) {
-        const float lp = kLn2 * (fmaf(x, kLog2e, -c1) - l1);
-        v += w1 * (i == tgt ? expm1f(lp) : expf(lp));
-      }
-      if (soft) v += wt * (ex2(fmaf(x, itl, -ct) - lt) - qs);
-      d[i] = __float2bfloat16_rn(v);
-    }
+    named_arrive<2>(CT + 32);
   }
 }
 
@@ -1101,58 +1172,43 @@ cudaError_t share_memory_config() {
   return e;
 }
 
-// Clusters of a distillation kernel that are resident at once, looked up once
-// per device, form, cluster size and slot room.
-template <int NV, int NT, bool TWO>
-cudaError_t distill_resident(int cluster, int kcap, int* out) {
+// Blocks of a distillation kernel that are resident at once, looked up once per
+// device, form and slot room.
+template <int CW, int NS, int BPS, bool TWO>
+cudaError_t distill_resident(int kcap, int* out) {
   constexpr int DEV = 16;
-  static std::atomic<int> known[DEV][4][6];
-  int dev = 0;
+  static std::atomic<int> known[DEV][6];
+  int dev = 0, ki = 0, sms = 0, n = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  int ci = 0, ki = 0;
-  while ((1 << ci) < cluster) ++ci;
   while ((32 << ki) < kcap) ++ki;
-  std::atomic<int>* slot = dev < DEV ? &known[dev][ci][ki] : nullptr;
+  std::atomic<int>* slot = dev < DEV ? &known[dev][ki] : nullptr;
   if (slot && (*out = slot->load(std::memory_order_acquire)) > 0) return cudaSuccess;
-  const size_t smem = kd_smem<NV, NT>(kcap);
   // room for the most slots, so that the setting never shrinks under another call
-  e = cudaFuncSetAttribute(distill_k<NV, NT, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)kd_smem<NV, NT>(KD_MAX_K));
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(cluster * 1024));
-  cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  e = cudaOccupancyMaxActiveClusters(&n, distill_k<NV, NT, TWO>, &cfg);
+  e = cudaFuncSetAttribute(distill_k<CW, NS, BPS, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)kd_smem<CW, NS>(KD_MAX_K));
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess)
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, distill_k<CW, NS, BPS, TWO>, (CW + 2) * 32,
+                                                      kd_smem<CW, NS>(kcap));
   if (e != cudaSuccess) return e;
   if (n < 1) return cudaErrorInvalidConfiguration;
-  if (slot) slot->store(n, std::memory_order_release);
-  *out = n;
+  *out = n * sms;
+  if (slot) slot->store(*out, std::memory_order_release);
   return cudaSuccess;
 }
 
-template <int NV, int NT, bool TWO>
-cudaError_t launch_distill2(const KdArgs& a, int cluster, cudaStream_t s) {
+template <int CW, int NS, int BPS, bool TWO>
+cudaError_t launch_distill2(const KdArgs& a, cudaStream_t s) {
   int n = 0;
-  const cudaError_t e = distill_resident<NV, NT, TWO>(cluster, a.kcap, &n);
+  const cudaError_t e = distill_resident<CW, NS, BPS, TWO>(a.kcap, &n);
   if (e != cudaSuccess) return e;
   if (n > a.rows) n = (int)a.rows;
-  return launch(distill_k<NV, NT, TWO>, dim3((unsigned)(n * cluster)), NT, kd_smem<NV, NT>(a.kcap), cluster, false, s,
-                a);
+  return launch(distill_k<CW, NS, BPS, TWO>, dim3((unsigned)n), (CW + 2) * 32, kd_smem<CW, NS>(a.kcap), 0, false, s, a);
 }
-template <int NV, int NT = 256>
-cudaError_t launch_distill(const KdArgs& a, int cluster, cudaStream_t s) {
-  return a.target && a.tau != 1.f ? launch_distill2<NV, NT, true>(a, cluster, s)
-                                  : launch_distill2<NV, NT, false>(a, cluster, s);
+template <int CW, int NS, int BPS>
+cudaError_t launch_distill(const KdArgs& a, cudaStream_t s) {
+  return a.target && a.tau != 1.f ? launch_distill2<CW, NS, BPS, true>(a, s) : launch_distill2<CW, NS, BPS, false>(a, s);
 }
 
 }  // namespace
@@ -1218,32 +1274,21 @@ cudaError_t distill_topk(const bf16* logits, const int32_t* target, const float*
   if (rows < 0 || rows > 0x7fffffff || V < 1 || K < 1 || K > KD_MAX_K || !(tau > 0.f) || !(tau < INFINITY) || !(1.f / tau < INFINITY) || !al16(logits) ||
       !al16(dlogits))
     return cudaErrorInvalidValue;
-  if (V > KD_MAX_V) return cudaErrorInvalidValue;
   if (rows == 0) return cudaSuccess;
   int kcap = 32;
   while (kcap < K) kcap *= 2;
   const KdArgs a{rows, kcap, logits, target, t_val, t_idx, V, K, tau, w_ce, w_kd, row_ce, row_kd, dlogits};
-  const int nvec = V / 8;  // whole vectors of a row at most
-  // blocks of a cluster so that a thread holds up to 9 vectors (more at the
-  // widest rows, where the cluster is at its largest)
-  int cluster = 1;
-  while (cluster < KD_MAX_CLUSTER && (nvec + cluster - 1) / cluster > 9 * 224) cluster *= 2;
-  const int per = (nvec + cluster - 1) / cluster;
-  switch ((per + 223) / 224) {
-    case 0: case 1: return launch_distill<1>(a, cluster, s);
-    case 2: return launch_distill<2>(a, cluster, s);
-    case 3: return launch_distill<3>(a, cluster, s);
-    case 4: return launch_distill<4>(a, cluster, s);
-    case 5: return launch_distill<5>(a, cluster, s);
-    case 6: return launch_distill<6>(a, cluster, s);
-    case 7: return launch_distill<7>(a, cluster, s);
-    case 8: return launch_distill<8>(a, cluster, s);
-    case 9: return launch_distill<9>(a, cluster, s);
-    case 10: case 11: return launch_distill<11>(a, cluster, s);
-    case 12: case 13: return launch_distill<13>(a, cluster, s);
-    case 14: case 15: return launch_distill<15>(a, cluster, s);
-    default: return launch_distill<KD_WIDE_NV, 512>(a, cluster, s);
-  }
+  // working warps by the row's length, each rule with both sides measured (us,
+  // GB300): one warp and 12 blocks per SM up to 12288 columns (8192 rows of
+  // 12288: 88 against 95 with four warps; of 16384: 125 against 102); four warps
+  // up to 24576 (of 24576: 157 against 183 with eight; of 28000: 177 against
+  // 170); eight up to 65536 (4096 rows of 64000: 196 against 209 with sixteen;
+  // of 80000: 252 against 214, where two rows per SM no longer stay in L2 until
+  // they are read again)
+  if (V <= 12288) return launch_distill<1, 6, 12>(a, s);
+  if (V <= 24576) return launch_distill<4, 6, 4>(a, s);
+  if (V <= 65536) return launch_distill<8, 6, 2>(a, s);
+  return launch_distill<16, 5, 1>(a, s);
 }
 
 size_t router_balance_scratch(int64_t T, int S, int E) {

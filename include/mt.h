@@ -477,8 +477,8 @@ mt_status mt_linear_cross_entropy(const void* h, const void* W, const int32_t* t
  * only; may be logits itself).  An id in several slots counts with the sum of
  * its q.  A row with no filled slot (or none above -inf) has no teacher part,
  * a target outside [0, V) no hard part; a row with neither gets zeros.
- * row_ce may be null.  V <= 524288, 1 <= K <= 1024, tau and 1 / tau
- * finite and > 0, logits and dlogits 16-byte aligned, else MT_ERR_ARG. */
+ * row_ce may be null.  1 <= K <= 1024, tau and 1 / tau finite and > 0,
+ * logits and dlogits 16-byte aligned, else MT_ERR_ARG; V may be odd. */
 mt_status mt_distill_topk(const void* logits, const int32_t* target, const float* t_val, const int32_t* t_idx,
                           int64_t rows, int32_t V, int32_t K, float tau, float w_ce, float w_kd, float* row_ce,
                           float* row_kd, void* dlogits, void* stream);
