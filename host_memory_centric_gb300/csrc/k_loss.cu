@@ -802,10 +802,19 @@ struct BalArgs {
 };
 
 // LPR lanes share a row, each holding NV vectors of 8 logits (vector j of a
-// lane: elements 8 (j LPR + lane) ..); VEC: E is a multiple of 8 and rows are
-// read and written as 16-byte vectors.  A block takes a.rows rows of one group;
-// the block that finishes a group last adds the blocks' sums in block order,
-// and the one that finishes the last group adds the groups' losses.
+// lane: elements 8 (j LPR + lane) ..).  A block takes a.rows rows of one group,
+// as many at a time as it has lanes for.  VEC: E is a multiple of 8; rows are
+// written as 16-byte vectors and come through a ring of BAL_STAGES chunks of
+// shared memory, filled by bulk copies (one register set ahead, a block had 16
+// KB on its way and an SM 4 of the 7 TB/s' worth; the ring holds four times
+// that).  The block that finishes a group last adds the blocks' sums in block
+// order, and the one that finishes the last group adds the groups' losses.
+constexpr int BAL_STAGES = 4;
+
+// Lanes that share a row, vectors a lane holds, rows a block has at a time.
+constexpr int bal_lanes(int E) { return E <= 8 ? 1 : E <= 16 ? 2 : E <= 32 ? 4 : E <= 64 ? 8 : E <= 128 ? 16 : 32; }
+constexpr int bal_rows(int E) { return BAL_THREADS / bal_lanes(E); }
+
 template <int LPR, int NV, bool VEC>
 __global__ void __launch_bounds__(BAL_THREADS, NV == 1 ? 2 : 1) balance_grad_k(const BalArgs a) {
   constexpr int RPB = BAL_THREADS / LPR;  // rows in flight per block
@@ -816,30 +825,56 @@ __global__ void __launch_bounds__(BAL_THREADS, NV == 1 ? 2 : 1) balance_grad_k(c
   __shared__ float red[WARPS];
   __shared__ int last;
   __shared__ int cnt[NE + 1];  // the group's choices per expert, its valid tokens at E
+  extern __shared__ __align__(128) float ring[];  // VEC: [BAL_STAGES][RPB][E]
+  __shared__ uint64_t full[BAL_STAGES];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sub = tid % LPR, slot = tid / LPR;
   const int64_t g = blockIdx.y;
   const int E = a.E;
   const int r1 = min(a.S, (int)(blockIdx.x + 1) * a.rows);
-  float x[NV * 8], f[NV * 8], P[NV * 8], zz = 0.f;
-  bool on;
-  auto load = [&](int r) {
-    const int64_t t = g * a.S + r;
-    on = r < r1 && (!a.valid || a.valid[t]);
+  const int first = (int)blockIdx.x * a.rows + slot;
+  constexpr int NP = NV * 4;  // pairs of columns a lane holds
+  f32x2 x[NP], f[NP], P[NP];
+  float zz = 0.f;
+  const int r0 = (int)blockIdx.x * a.rows, chunks = (r1 - r0 + RPB - 1) / RPB;
+  const float* src = a.logits + (g * a.S + first) * E + sub * 8;
+  bf16* dst = a.dlogits + (g * a.S + first) * E + sub * 8;
+  const uint8_t* val = a.valid ? a.valid + g * a.S + first : nullptr;
+  bool failed = false;
+  auto fill = [&](int c) {  // one thread: chunk c into its stage of the ring
+    const uint32_t bytes = (uint32_t)min(RPB, r1 - r0 - c * RPB) * (uint32_t)E * 4;
+    mbar_expect_tx(&full[c % BAL_STAGES], bytes);
+    bulk_load(ring + (c % BAL_STAGES) * RPB * E, a.logits + (g * a.S + r0 + c * RPB) * E, bytes, &full[c % BAL_STAGES]);
+  };
+  if (VEC) {
+    if (tid == 0) {
+      for (int i = 0; i < BAL_STAGES; ++i) mbar_init(&full[i], 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      for (int c = 0; c < min(chunks, BAL_STAGES); ++c) fill(c);
+    }
+    __syncthreads();
+  }
+  const f32x2 nothing = pair2(-INFINITY, -INFINITY);
+  auto load = [&](int c, bool on) {  // this lane's part of its row of chunk c
+    const float* in = VEC ? ring + ((c % BAL_STAGES) * RPB + slot) * E + sub * 8 : src;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int e = (j * LPR + sub) * 8;
       if (VEC) {
-        float4 u = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY), w = u;
+        x[4 * j] = x[4 * j + 1] = x[4 * j + 2] = x[4 * j + 3] = nothing;
         if (on && e < E) {
-          u = *reinterpret_cast<const float4*>(a.logits + t * E + e);
-          w = *reinterpret_cast<const float4*>(a.logits + t * E + e + 4);
+          const ulonglong2* p = reinterpret_cast<const ulonglong2*>(in + j * LPR * 8);
+          const ulonglong2 u = p[0], w = p[1];
+          x[4 * j] = u.x;
+          x[4 * j + 1] = u.y;
+          x[4 * j + 2] = w.x;
+          x[4 * j + 3] = w.y;
         }
-        x[8 * j] = u.x; x[8 * j + 1] = u.y; x[8 * j + 2] = u.z; x[8 * j + 3] = u.w;
-        x[8 * j + 4] = w.x; x[8 * j + 5] = w.y; x[8 * j + 6] = w.z; x[8 * j + 7] = w.w;
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[8 * j + i] = on && e + i < E ? a.logits[t * E + e + i] : -INFINITY;
+        for (int i = 0; i < 4; ++i)
+          x[4 * j + i] = pair2(on && e + 2 * i < E ? in[j * LPR * 8 + 2 * i] : -INFINITY,
+                               on && e + 2 * i + 1 < E ? in[j * LPR * 8 + 2 * i + 1] : -INFINITY);
       }
     }
   };
@@ -851,26 +886,42 @@ __global__ void __launch_bounds__(BAL_THREADS, NV == 1 ? 2 : 1) balance_grad_k(c
   auto sum = [](float u, float w) { return u + w; };
   auto mx = [](float u, float w) { return fmaxf(u, w); };
 #pragma unroll
-  for (int i = 0; i < NV * 8; ++i) P[i] = f[i] = 0.f;
-  int r = (int)blockIdx.x * a.rows + slot;
-  load(r);
-  float cb = 0.f, cz = 0.f, inv_n = 0.f;
+  for (int i = 0; i < NP; ++i) P[i] = f[i] = 0;
+  float cz = 0.f, cb = 0.f, inv_n = 0.f;
   bool started = false;
+  const f32x2 l2e = pair2(kLog2e, kLog2e);
+  constexpr float kLn2 = 0.6931471805599453f;
+  int r = first;
+  bool on = r < r1 && (!val || *val);
   // the same number of turns for every lane of a warp: the shuffles are warp-wide
-  for (int base = (int)blockIdx.x * a.rows; base < r1; base += RPB, r += RPB) {
+  for (int turn = 0; turn < chunks; ++turn, r += RPB) {
     const bool now = on;
-    float m = -INFINITY, s = 0.f, fe = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV * 8; ++i) m = fmaxf(m, x[i]);
-    m = over_row(m, mx);
-    float e8[NV * 8];
-#pragma unroll
-    for (int i = 0; i < NV * 8; ++i) {
-      e8[i] = ex2((x[i] - m) * kLog2e);  // 0 beyond E, where x is -inf
-      s += e8[i];
+    if (VEC) mbar_wait(&full[turn % BAL_STAGES], (uint32_t)(turn / BAL_STAGES) & 1, failed);
+    load(turn, now);
+    if (VEC) {
+      __syncthreads();  // every lane has its part: the stage takes the next chunk
+      if (tid == 0 && turn + BAL_STAGES < chunks) fill(turn + BAL_STAGES);
     }
-    const bool pad_lanes = !now;  // rows outside the block or padded: nothing below counts
-    load(r + RPB);                // the next row is on its way while this one is worked on
+    src += (int64_t)RPB * E;
+    if (val) val += RPB;
+    on = r + RPB < r1 && (!val || *val);
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const float2 t = unpair2(x[i]);
+      m = fmaxf(m, fmaxf(t.x, t.y));
+    }
+    m = over_row(m, mx);
+    // 2^(x log2(e) - c) with c = fl(m log2(e)): the rounding of c cancels.  Padded
+    // rows and lanes beyond E hold -inf, whose exponential is 0.
+    const float c = m == -INFINITY ? 0.f : __fmul_rn(m, kLog2e);
+    const f32x2 nc = pair2(-c, -c);
+    f32x2 e2[NP], s2 = 0, f2 = 0;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      e2[i] = ex2_2(fma2(x[i], l2e, nc));
+      s2 = add2(s2, e2[i]);
+    }
     if (!started) {
       started = true;
       dep_wait();  // the counts and the tickets
@@ -880,10 +931,10 @@ __global__ void __launch_bounds__(BAL_THREADS, NV == 1 ? 2 : 1) balance_grad_k(c
       const int lanes = max(1, BAL_THREADS / (E + 1));  // threads that share a column, each taking every lanes-th part
       for (int i = tid; i < lanes * (E + 1); i += BAL_THREADS) {
         const int e = i % (E + 1);
-        int c = 0;
+        int n = 0;
 #pragma unroll 8
-        for (int q = i / (E + 1); q < a.nparts; q += lanes) c += pc[q * a.ldp + e];
-        atomicAdd(&cnt[e], c);
+        for (int q = i / (E + 1); q < a.nparts; q += lanes) n += pc[q * a.ldp + e];
+        atomicAdd(&cnt[e], n);
       }
       __syncthreads();
       const int n = cnt[E];
@@ -893,88 +944,99 @@ __global__ void __launch_bounds__(BAL_THREADS, NV == 1 ? 2 : 1) balance_grad_k(c
       cb = a.alpha * (float)E * inv_n;
       cz = 2.f * a.z_coef * inv_n;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = (j * LPR + sub) * 8 + i;
-          if (e < E) f[8 * j + i] = (float)cnt[e] * inv_n / (float)a.k;
-        }
+      for (int i = 0; i < NP; ++i) {
+        const int e = ((i >> 2) * LPR + sub) * 8 + 2 * (i & 3);
+        f[i] = pair2(e < E ? (float)cnt[e] * inv_n / (float)a.k : 0.f,
+                     e + 1 < E ? (float)cnt[e + 1] * inv_n / (float)a.k : 0.f);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < NV * 8; ++i) fe += f[i] * e8[i];
-    s = over_row(s, sum);
-    fe = over_row(fe, sum);
-    const float is = 1.f / s, lse = m + logf(s), mean = fe * is, shift = cz * lse - cb * mean;
-    if (!pad_lanes) {
+    for (int i = 0; i < NP; ++i) f2 = fma2(f[i], e2[i], f2);
+    const float2 st = unpair2(s2), ft = unpair2(f2);
+    const float s = over_row(st.x + st.y, sum), fe = over_row(ft.x + ft.y, sum);
+    const float is = now ? __fdividef(1.f, s) : 0.f;
+    const float lse = now ? kLn2 * (__log2f(s) + c) : 0.f;
+    const float shift = cz * lse - cb * (fe * is);
+    const f32x2 is2 = pair2(is, is), cb2 = pair2(cb, cb), sh2 = pair2(shift, shift);
+    if (sub == 0) zz += lse * lse;
+    uint32_t o[NP];
 #pragma unroll
-      for (int i = 0; i < NV * 8; ++i) {
-        const float p = e8[i] * is;
-        P[i] += p;
-        e8[i] = p * (cb * f[i] + shift);
-      }
-      if (sub == 0) zz += lse * lse;
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV * 8; ++i) e8[i] = 0.f;
+    for (int i = 0; i < NP; ++i) {
+      const f32x2 p = mul2(e2[i], is2);
+      P[i] = add2(P[i], p);
+      const float2 t = unpair2(mul2(p, fma2(f[i], cb2, sh2)));
+      const __nv_bfloat162 h = __floats2bfloat162_rn(t.x, t.y);
+      o[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
     if (a.dlogits && r < r1) {
-      bf16* d = a.dlogits + (g * a.S + r) * E;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int e = (j * LPR + sub) * 8;
         if (VEC) {
-          if (e < E) {
-            float o8[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o8[i] = e8[8 * j + i];
-            *reinterpret_cast<uint4*>(d + e) = pack8(o8);
-          }
+          if (e < E)
+            *reinterpret_cast<uint4*>(dst + j * LPR * 8) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (e + i < E) d[e + i] = __float2bfloat16_rn(e8[8 * j + i]);
+            if (e + i < E)
+              dst[j * LPR * 8 + i] = __ushort_as_bfloat16((unsigned short)(o[4 * j + (i >> 1)] >> (16 * (i & 1))));
         }
       }
+    }
+    dst += (int64_t)RPB * E;
+  }
+  if (VEC && failed && tid == 0) {  // what is on its way lands before the block's memory goes
+    const long long t0 = clock64();
+    while (clock64() - t0 < kWaitCycles) {
     }
   }
   // the block's sums: rows of a warp by shuffles, warps in warp order
 #pragma unroll
-  for (int i = 0; i < NV * 8; ++i) {
+  for (int i = 0; i < NP; ++i) {
 #pragma unroll
-    for (int o = 16; o >= LPR; o >>= 1) P[i] += __shfl_xor_sync(0xffffffffu, P[i], o);
-    if (lane < LPR) acc[warp][((i >> 3) * LPR + sub) * 8 + (i & 7)] = P[i];
+    for (int o = 16; o >= LPR; o >>= 1) P[i] = add2(P[i], __shfl_xor_sync(0xffffffffu, P[i], o));
+    const float2 t = unpair2(P[i]);
+    if (lane < LPR) {
+      acc[warp][((i >> 2) * LPR + sub) * 8 + 2 * (i & 3)] = t.x;
+      acc[warp][((i >> 2) * LPR + sub) * 8 + 2 * (i & 3) + 1] = t.y;
+    }
   }
   zz = warp_sum(zz);
   if (lane == 0) acc[warp][NE] = zz;
   __syncthreads();
-  float* part = a.partial + (g * a.nblk + blockIdx.x) * a.ldp;
+  // (a group of one block has its sums at hand: no trip through memory)
+  float* part = a.nblk == 1 ? tree : a.partial + (g * a.nblk + blockIdx.x) * a.ldp;
   for (int e = tid; e < a.ldp; e += BAL_THREADS) {
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) v += e <= E ? acc[w][e < E ? e : NE] : 0.f;
     part[e] = v;
   }
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) last = atomicAdd(&a.ticket[1 + g], 1) == a.nblk - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  // the group: thread (c, q) adds the four columns q of blocks c, c + C, ... in order, then the C parts in order
-  const int c4 = a.ldp / 4, C = max(1, min(a.nblk, BAL_THREADS / c4));
-  const float4* all = reinterpret_cast<const float4*>(a.partial + g * a.nblk * a.ldp);
-  if (tid < C * c4) {
-    const int c = tid / c4, q = tid % c4;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  int C = 1;
+  if (a.nblk > 1) {
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) last = atomicAdd(&a.ticket[1 + g], 1) == a.nblk - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    // the group: thread (c, q) adds the four columns q of blocks c, c + C, ... in order, then the C parts in order
+    const int c4 = a.ldp / 4;
+    C = max(1, min(a.nblk, BAL_THREADS / c4));
+    const float4* all = reinterpret_cast<const float4*>(a.partial + g * a.nblk * a.ldp);
+    if (tid < C * c4) {
+      const int c = tid / c4, q = tid % c4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int b = c; b < a.nblk; b += C) {
-      const float4 u = __ldcg(all + (int64_t)b * c4 + q);
-      v.x += u.x;
-      v.y += u.y;
-      v.z += u.z;
-      v.w += u.w;
+      for (int b = c; b < a.nblk; b += C) {
+        const float4 u = __ldcg(all + (int64_t)b * c4 + q);
+        v.x += u.x;
+        v.y += u.y;
+        v.z += u.z;
+        v.w += u.w;
+      }
+      reinterpret_cast<float4*>(tree)[tid] = v;
     }
-    reinterpret_cast<float4*>(tree)[tid] = v;
   }
   __syncthreads();
   float lb = 0.f, lz = 0.f;
@@ -991,22 +1053,24 @@ __global__ void __launch_bounds__(BAL_THREADS, NV == 1 ? 2 : 1) balance_grad_k(c
   }
   lb = block_sum<BAL_THREADS>(lb, red);
   lz = block_sum<BAL_THREADS>(lz, red);
-  if (tid == 0) {
-    a.gloss[g] = make_float2(lb, lz);
+  if (a.G > 1) {
+    if (tid == 0) {
+      a.gloss[g] = make_float2(lb, lz);
+      __threadfence();
+      last = atomicAdd(&a.ticket[0], 1) == a.G - 1;
+    }
+    __syncthreads();
+    if (!last) return;
     __threadfence();
-    last = atomicAdd(&a.ticket[0], 1) == a.G - 1;
+    lb = lz = 0.f;
+    for (int64_t i = tid; i < a.G; i += BAL_THREADS) {
+      const float2 v = __ldcg(a.gloss + i);
+      lb += v.x;
+      lz += v.y;
+    }
+    lb = block_sum<BAL_THREADS>(lb, red);
+    lz = block_sum<BAL_THREADS>(lz, red);
   }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  lb = lz = 0.f;
-  for (int64_t i = tid; i < a.G; i += BAL_THREADS) {
-    const float2 v = __ldcg(a.gloss + i);
-    lb += v.x;
-    lz += v.y;
-  }
-  lb = block_sum<BAL_THREADS>(lb, red);
-  lz = block_sum<BAL_THREADS>(lz, red);
   if (tid == 0) {
     a.loss[0] = lb * a.alpha * (float)E;
     a.loss[1] = lz * a.z_coef;
@@ -1102,7 +1166,7 @@ size_t bal_carve(int64_t T, int S, int E, uint8_t* base, BalScratch* w) {
   };
   const int64_t G = T / S;
   int64_t blk = (kBalBlocks + G - 1) / G;
-  const int64_t most = (S + 31) / 32;  // a block has at least 32 rows to take
+  const int64_t most = (S + bal_rows(E) - 1) / bal_rows(E);  // a block has all its lanes' rows to take
   if (blk > most) blk = most;
   w->rows = (int)((S + blk - 1) / blk);
   w->nblk = (S + w->rows - 1) / w->rows;
@@ -1151,8 +1215,21 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, in
 template <int LPR, int NV>
 cudaError_t launch_balance_grad(const BalArgs& a, cudaStream_t s) {
   const dim3 grid((unsigned)a.nblk, (unsigned)a.G);
-  return a.E % 8 == 0 ? launch(balance_grad_k<LPR, NV, true>, grid, BAL_THREADS, 0, 0, true, s, a)
-                      : launch(balance_grad_k<LPR, NV, false>, grid, BAL_THREADS, 0, 0, true, s, a);
+  if (a.E % 8) return launch(balance_grad_k<LPR, NV, false>, grid, BAL_THREADS, 0, 0, true, s, a);
+  constexpr int DEV = 16;
+  static std::atomic<int> done[DEV];  // room for the whole ring, set once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev >= DEV || !done[dev].load(std::memory_order_acquire))) {
+    e = cudaFuncSetAttribute(balance_grad_k<LPR, NV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(BAL_STAGES * (size_t)BAL_THREADS * NV * 32));
+    if (e == cudaSuccess && dev < DEV) done[dev].store(1, std::memory_order_release);
+  }
+  if (e != cudaSuccess) return e;
+  // no more stages than the block has chunks for
+  const int chunks = (a.rows + BAL_THREADS / LPR - 1) / (BAL_THREADS / LPR);
+  const size_t smem = (size_t)(BAL_THREADS / LPR) * a.E * 4 * (chunks < BAL_STAGES ? chunks : BAL_STAGES);
+  return launch(balance_grad_k<LPR, NV, true>, grid, BAL_THREADS, smem, 0, true, s, a);
 }
 
 // The join and the sum of runs stand between two GEMMs that use nearly all
