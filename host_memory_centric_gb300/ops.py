@@ -11,14 +11,20 @@ import ctypes as C
 import numpy as np
 
 
+_lib = None
+
+
 def _L():
-    from . import lib
-    return lib()
+    global _lib
+    if _lib is None:
+        from . import lib
+        _lib = lib()
+    return _lib
 
 
 def _chk(s):
-    from . import MtError
     if s != 0:
+        from . import MtError
         raise MtError(s, "device op failed")
 
 
@@ -155,23 +161,24 @@ def _device(name, t):
     return dev
 
 
-def _want(name, t, dtype, shape, dev):
-    """Refuses a tensor the library would misread: another type, shape, stride or device."""
+def _arg(name, t, dtype, shape, dev):
+    """Address of a tensor argument; refuses one the library would misread: another type, shape, stride or device."""
     if t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
         got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}"
         _refuse(f"{name}: want a contiguous {dtype} tensor of shape {shape} on CUDA device {dev}, got {got}")
+    return t.data_ptr()
+
+
+def _scratch(t, dev):
+    """Address and bytes of a workspace; the library itself refuses one that is too small."""
+    if t is None or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(f"scratch: want contiguous memory of CUDA device {dev}")
+    return t.data_ptr(), t.nbytes
 
 
 def _raw_stream(dev):
     import torch
     return torch._C._cuda_getCurrentRawStream(dev)  # _stream() without building a Stream object (3 us)
-
-
-def _scratch(t, dev):
-    """Bytes of a workspace; the library itself refuses one that is too small."""
-    if t is None or not t.is_contiguous() or t.get_device() != dev:
-        _refuse(f"scratch: want contiguous memory of CUDA device {dev}")
-    return t.numel() * t.element_size()
 
 
 def linear_cross_entropy_scratch_bytes(T, H, V, grads=True) -> int:
@@ -187,14 +194,12 @@ def linear_cross_entropy(h, W, target, inv_norm, row_loss, dh, dW, scratch):
     T, H = h.shape
     V = W.shape[0]
     dev = _device("h", h)
-    _want("h", h, bf, (T, H), dev); _want("W", W, bf, (V, H), dev); _want("target", target, torch.int32, (T,), dev)
-    _want("row_loss", row_loss, torch.float32, (T,), dev)
-    if dh is not None:
-        _want("dh", dh, bf, (T, H), dev)
-    if dW is not None:
-        _want("dW", dW, bf, (V, H), dev)
-    _chk(_L().mt_linear_cross_entropy(_p(h), _p(W), _p(target), T, H, V, inv_norm, _p(row_loss), _p(dh), _p(dW),
-                                      _p(scratch), _scratch(scratch, dev), _raw_stream(dev)))
+    ws, nbytes = _scratch(scratch, dev)
+    _chk(_L().mt_linear_cross_entropy(
+        _arg("h", h, bf, (T, H), dev), _arg("W", W, bf, (V, H), dev), _arg("target", target, torch.int32, (T,), dev),
+        T, H, V, inv_norm, _arg("row_loss", row_loss, torch.float32, (T,), dev),
+        None if dh is None else _arg("dh", dh, bf, (T, H), dev),
+        None if dW is None else _arg("dW", dW, bf, (V, H), dev), ws, nbytes, _raw_stream(dev)))
 
 
 def distill_topk(logits, target, t_val, t_idx, tau, w_ce, w_kd, row_ce, row_kd, dlogits):
@@ -202,19 +207,17 @@ def distill_topk(logits, target, t_val, t_idx, tau, w_ce, w_kd, row_ce, row_kd, 
     row_ce may be None (no hard targets), dlogits None (losses only) or logits
     itself."""
     import torch
+    f32, i32 = torch.float32, torch.int32
     rows, V = logits.shape
     K = t_val.shape[1]
     dev = _device("logits", logits)
-    _want("logits", logits, torch.bfloat16, (rows, V), dev); _want("row_kd", row_kd, torch.float32, (rows,), dev)
-    _want("t_val", t_val, torch.float32, (rows, K), dev); _want("t_idx", t_idx, torch.int32, (rows, K), dev)
-    if target is not None:
-        _want("target", target, torch.int32, (rows,), dev)
-    if row_ce is not None:
-        _want("row_ce", row_ce, torch.float32, (rows,), dev)
-    if dlogits is not None:
-        _want("dlogits", dlogits, torch.bfloat16, (rows, V), dev)
-    _chk(_L().mt_distill_topk(_p(logits), _p(target), _p(t_val), _p(t_idx), rows, V, K, tau, w_ce, w_kd, _p(row_ce),
-                              _p(row_kd), _p(dlogits), _raw_stream(dev)))
+    _chk(_L().mt_distill_topk(
+        _arg("logits", logits, torch.bfloat16, (rows, V), dev),
+        None if target is None else _arg("target", target, i32, (rows,), dev),
+        _arg("t_val", t_val, f32, (rows, K), dev), _arg("t_idx", t_idx, i32, (rows, K), dev), rows, V, K, tau, w_ce,
+        w_kd, None if row_ce is None else _arg("row_ce", row_ce, f32, (rows,), dev),
+        _arg("row_kd", row_kd, f32, (rows,), dev),
+        None if dlogits is None else _arg("dlogits", dlogits, torch.bfloat16, (rows, V), dev), _raw_stream(dev)))
 
 
 def router_balance_scratch_bytes(T, S, E) -> int:
@@ -226,21 +229,21 @@ def router_balance(logits, idx, valid, S, alpha, z_coef, loss, counts, prob, dlo
     probabilities per group and expert, gradient of the logits
     (mt_router_balance).  valid and dlogits may be None."""
     import torch
+    f32, i32 = torch.float32, torch.int32
     T, E = logits.shape
     k = idx.shape[1]
     if S < 1 or T % S:
         _refuse(f"{T} tokens are not groups of {S}")
     G = T // S
     dev = _device("logits", logits)
-    _want("logits", logits, torch.float32, (T, E), dev); _want("idx", idx, torch.int32, (T, k), dev)
-    _want("loss", loss, torch.float32, (2,), dev); _want("counts", counts, torch.int32, (G, E), dev)
-    _want("prob", prob, torch.float32, (G, E), dev)
-    if valid is not None:
-        _want("valid", valid, torch.uint8, (T,), dev)
-    if dlogits is not None:
-        _want("dlogits", dlogits, torch.bfloat16, (T, E), dev)
-    _chk(_L().mt_router_balance(_p(logits), _p(idx), _p(valid), T, S, E, k, alpha, z_coef, _p(loss), _p(counts),
-                                _p(prob), _p(dlogits), _p(scratch), _scratch(scratch, dev), _raw_stream(dev)))
+    ws, nbytes = _scratch(scratch, dev)
+    _chk(_L().mt_router_balance(
+        _arg("logits", logits, f32, (T, E), dev), _arg("idx", idx, i32, (T, k), dev),
+        None if valid is None else _arg("valid", valid, torch.uint8, (T,), dev), T, S, E, k, alpha, z_coef,
+        _arg("loss", loss, f32, (2,), dev), _arg("counts", counts, i32, (G, E), dev),
+        _arg("prob", prob, f32, (G, E), dev),
+        None if dlogits is None else _arg("dlogits", dlogits, torch.bfloat16, (T, E), dev), ws, nbytes,
+        _raw_stream(dev)))
 
 
 def moe_scratch_bytes(T, H, E, k, Fe):
