@@ -65,138 +65,8 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   return t;
 }
 
-// A kernel launched with programmatic serialisation may start while the one
-// before it runs; it sees that one's writes after dep_wait().
-__device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-// ------------------------------------------------------------------ linear cross-entropy
-// One block per row: joins the row's pieces (m_p, s_p), whose sums leave the
-// target out, with M = max m_p:
-//   rest = sum_p s_p exp(m_p - M),  S = rest + exp(z_target - M),
-//   loss = (M - z_target) + log S,
-// and, with E, turns the stored fp16 2^15 exp(z - m_p) into the logits'
-// gradient in BF16 in place: d = exp(z - m_p) exp(m_p - M) / S, one factor per
-// piece of 128 columns, and d = -rest / S (= p - 1) at the target, so that loss
-// and gradient of a confident row (p near 1) keep their digits.  The factor g
-// of the gradients waits for the products' FP32 results: rounded here, g (p - 1)
-// of most rows would be off by the same amount, and the errors would add up.
-// Rows without a target get zeros.  Bound by HBM (4 bytes a logit).  The blocks
-// of grid.y share a row; each joins the statistics for itself.
-constexpr int JOIN_THREADS = 256;
-
-__global__ void __launch_bounds__(JOIN_THREADS) ce_join_k(const float2* __restrict__ stat, int npieces,
-                                                          const int32_t* __restrict__ target,
-                                                          const float* __restrict__ zt, int V,
-                                                          float* __restrict__ row_loss, uint16_t* __restrict__ E,
-                                                          int64_t ldE) {
-  __shared__ float red[JOIN_THREADS / 32];
-  dep_launch();
-  dep_wait();
-  const int64_t row = blockIdx.x;
-  const int tgt = target[row];
-  const bool has = tgt >= 0 && tgt < V;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint4* e = reinterpret_cast<uint4*>(E + row * ldE);
-  const int nvec = (V + 7) / 8, step = 32 * (JOIN_THREADS / 32) * (int)gridDim.y;
-  const int first = ((int)blockIdx.y * (JOIN_THREADS / 32) + warp) * 32 + lane;
-  if (!has) {
-    if (threadIdx.x == 0 && blockIdx.y == 0) row_loss[row] = 0.f;
-    if (E)
-      for (int v = first; v < nvec; v += step) e[v] = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  const float2* st = stat + row * npieces;
-  float m = -INFINITY;
-  for (int p = threadIdx.x; p < npieces; p += JOIN_THREADS) m = fmaxf(m, st[p].x);
-  const float M = block_max<JOIN_THREADS>(m, red);
-  float s = 0.f;
-  for (int p = threadIdx.x; p < npieces; p += JOIN_THREADS) s += st[p].y * expf(st[p].x - M);
-  const float rest = block_sum<JOIN_THREADS>(s, red);
-  const float z = zt[row], et = expf(z - M), S = rest + et;
-  if (threadIdx.x == 0 && blockIdx.y == 0) row_loss[row] = z == M ? log1pf(rest) : (M - z) + logf(S);
-  if (!E) return;
-  const float scale = 0x1p-15f / S, dt = -rest / S;
-  constexpr int U = 4;  // vectors of a thread on their way at a time
-  for (int v = first; v < nvec; v += U * step) {
-    uint4 q[U];
-    float f[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int w = v + u * step;
-      if (w < nvec) {
-        q[u] = e[w];
-        f[u] = st[w >> 4].x;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int w = v + u * step;
-      if (w >= nvec) continue;
-      const float k = expf(f[u] - M) * scale;
-      const __half2* h = reinterpret_cast<const __half2*>(&q[u]);
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 t = __half22float2(h[i]);
-        x[2 * i] = t.x * k;
-        x[2 * i + 1] = t.y * k;
-      }
-      if (w == tgt >> 3) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (w * 8 + i == tgt) x[i] = dt;
-      }
-      e[w] = pack8(x);
-    }
-  }
-}
-
-// dh = bf16(g sum over the runs of a split sum), n4 groups of four values.
-__global__ void __launch_bounds__(256) ce_add_runs_k(const float4* __restrict__ slabs, int64_t n4, int runs, float g,
-                                                     uint2* __restrict__ dh) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  dep_launch();
-  dep_wait();
-  if (i >= n4) return;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int r = 0; r < runs; ++r) {
-    const float4 u = slabs[r * n4 + i];
-    v.x += u.x;
-    v.y += u.y;
-    v.z += u.z;
-    v.w += u.w;
-  }
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * g, v.y * g), b = __floats2bfloat162_rn(v.z * g, v.w * g);
-  dh[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
-
-// ------------------------------------------------------------------ cluster helpers
 __device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// shared::cluster address of the object at the same offset in CTA `rank`
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(su32(p)), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
+
 constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -204,39 +74,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// ------------------------------------------------------------------ distillation
-// A row of student logits z, teacher logits y at ids i:
-//   q = softmax over the filled slots of y / tau, p = softmax(z / tau),
-//   kd = sum_j q_j (log q_j - log p_{i_j}),  ce = lse(z) - z_target,
-//   dz_v = w_ce (softmax(z)_v - [v = target]) + w_kd / tau (p_v - sum_{i_j = v} q_j).
-// Bound by HBM: the statistics need the whole row before the first gradient
-// element.  A block takes one row at a time, and every n-th row: a producer
-// lane streams the row through a ring of shared memory with bulk copies, always
-// ahead of the warps that work on it, across row ends.  Where a row fits the
-// ring it stays there until its gradient is written; a longer one is fetched a
-// second time, from L2 (152 rows under work are at most 46 MB of 152064
-// columns).  The working warps take running sums of exp(z - m) around each
-// thread's maximum m at both temperatures, join them once per row, and write
-// the dense part of the gradient.  A further warp works out the teacher's
-// distribution of the next row meanwhile, and rewrites the at most K + 1
-// columns with a teacher entry or the target from their FP32 values once the
-// dense part stands, so that no element is rounded twice and an id that appears
-// in several slots gets the sum of their q, in slot order.
-constexpr int KD_MAX_K = 1024;
-constexpr int KD_U = 4;  // 16-byte vectors of a thread per chunk of the ring
-
-struct KdArgs {
-  int64_t rows;
-  int kcap;  // slots there is room for: K up to a power of two, at least 32
-  const bf16* logits;
-  const int32_t* target;
-  const float* t_val;
-  const int32_t* t_idx;
-  int V, K;
-  float tau, w_ce, w_kd;
-  float *row_ce, *row_kd;
-  bf16* dlogits;
-};
+// A kernel launched with programmatic serialisation may start while the one
+// before it runs; it sees that one's writes after dep_wait().
+__device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Two FP32 values in a register pair: one instruction for both
 // (fma / add / mul.f32x2), each rounded as the single form rounds it.
@@ -321,6 +162,421 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t n
 __device__ __forceinline__ void async_load4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(su32(dst)), "l"(src) : "memory");
 }
+
+// ------------------------------------------------------------------ linear cross-entropy
+// One block per row: joins the row's pieces (m_p, s_p), whose sums leave the
+// target out, with M = max m_p:
+//   rest = sum_p s_p exp(m_p - M),  S = rest + exp(z_target - M),
+//   loss = (M - z_target) + log S,
+// and, with E, turns the stored fp16 2^15 exp(z - m_p) into the logits'
+// gradient in BF16 in place: d = exp(z - m_p) exp(m_p - M) / S, one factor per
+// piece of 128 columns, and d = -rest / S (= p - 1) at the target, so that loss
+// and gradient of a confident row (p near 1) keep their digits.  The factor g
+// of the gradients waits for the products' FP32 results: rounded here, g (p - 1)
+// of most rows would be off by the same amount, and the errors would add up.
+// Rows without a target get zeros.  Bound by HBM (4 bytes a logit).  The blocks
+// of grid.y share a row; each joins the statistics for itself.
+constexpr int JOIN_THREADS = 256;
+
+__global__ void __launch_bounds__(JOIN_THREADS) ce_join_k(const float2* __restrict__ stat, int npieces,
+                                                          const int32_t* __restrict__ target,
+                                                          const float* __restrict__ zt, int V,
+                                                          float* __restrict__ row_loss, uint16_t* __restrict__ E,
+                                                          int64_t ldE) {
+  __shared__ float red[JOIN_THREADS / 32];
+  dep_launch();
+  dep_wait();
+  const int64_t row = blockIdx.x;
+  const int tgt = target[row];
+  const bool has = tgt >= 0 && tgt < V;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint4* e = reinterpret_cast<uint4*>(E + row * ldE);
+  const int nvec = (V + 7) / 8, step = 32 * (JOIN_THREADS / 32) * (int)gridDim.y;
+  const int first = ((int)blockIdx.y * (JOIN_THREADS / 32) + warp) * 32 + lane;
+  if (!has) {
+    if (threadIdx.x == 0 && blockIdx.y == 0) row_loss[row] = 0.f;
+    if (E)
+      for (int v = first; v < nvec; v += step) e[v] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const float2* st = stat + row * npieces;
+  float m = -INFINITY;
+  for (int p = threadIdx.x; p < npieces; p += JOIN_THREADS) m = fmaxf(m, st[p].x);
+  const float M = block_max<JOIN_THREADS>(m, red);
+  float s = 0.f;
+  for (int p = threadIdx.x; p < npieces; p += JOIN_THREADS) s += st[p].y * expf(st[p].x - M);
+  const float rest = block_sum<JOIN_THREADS>(s, red);
+  const float z = zt[row], et = expf(z - M), S = rest + et;
+  if (threadIdx.x == 0 && blockIdx.y == 0) row_loss[row] = z == M ? log1pf(rest) : (M - z) + logf(S);
+  if (!E) return;
+  const float scale = 0x1p-15f / S, dt = -rest / S;
+  constexpr int U = 4;  // vectors of a thread on their way at a time
+  for (int v = first; v < nvec; v += U * step) {
+    uint4 q[U];
+    float f[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int w = v + u * step;
+      if (w < nvec) {
+        q[u] = e[w];
+        f[u] = st[w >> 4].x;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int w = v + u * step;
+      if (w >= nvec) continue;
+      const float k = expf(f[u] - M) * scale;
+      const __half2* h = reinterpret_cast<const __half2*>(&q[u]);
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 t = __half22float2(h[i]);
+        x[2 * i] = t.x * k;
+        x[2 * i + 1] = t.y * k;
+      }
+      if (w == tgt >> 3) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (w * 8 + i == tgt) x[i] = dt;
+      }
+      e[w] = pack8(x);
+    }
+  }
+}
+
+// dh = bf16(g sum over the runs of a split sum), n4 groups of four values; the
+// eight warps of a block take every eighth run, their sums join in warp order.
+__global__ void __launch_bounds__(256) ce_add_runs_k(const float4* __restrict__ slabs, int64_t n4, int runs, float g,
+                                                     uint2* __restrict__ dh) {
+  __shared__ float4 part[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t i = (int64_t)blockIdx.x * 32 + lane;
+  dep_launch();
+  dep_wait();
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (i < n4) {
+#pragma unroll 4
+    for (int r = warp; r < runs; r += 8) {
+      const float4 u = slabs[r * n4 + i];
+      v.x += u.x;
+      v.y += u.y;
+      v.z += u.z;
+      v.w += u.w;
+    }
+  }
+  part[warp][lane] = v;
+  __syncthreads();
+  if (warp != 0 || i >= n4) return;
+#pragma unroll
+  for (int w = 1; w < 8; ++w) {
+    const float4 u = part[w][lane];
+    v.x += u.x;
+    v.y += u.y;
+    v.z += u.z;
+    v.w += u.w;
+  }
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * g, v.y * g), b = __floats2bfloat162_rn(v.z * g, v.w * g);
+  dh[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// Up to eight tokens.  The products are then bound by reading W twice and
+// writing dW once, and their tiles' fixed costs weigh more than their work: of
+// a 256-row tile three per cent would be tokens, and one head of 448 by 93899
+// took 137 us of which the bytes need 25.  So W is streamed through registers:
+//   forward: z = h W^T by mma.sync (16 by 8 by 16, half of its rows used), one
+//   warp on 16 rows of W, h in shared memory; z goes to scratch in FP32 (8 rows
+//   at most) beside each block's (m, s) as in softmax_piece;
+//   backward: one thread per 4 columns of W; for every row it adds d_v W_v to
+//   its part of dh and writes dW_v = g sum_t d_tv h_t, tokens in pairs
+//   (fma.f32x2), d in FP32: no rounding but the outputs'.
+constexpr int FEW_T = 8, FEW_WARPS = 8, FEW_ROWS = FEW_WARPS * 16;
+constexpr int FEW_MAX_H = 12000;  // h in shared memory: 8 rows of up to 24 KB
+// bytes of a row of h in shared memory: whole 64-byte groups, an odd number of
+// them, so that the rows an LDS.128 touches at once lie in different banks
+__host__ __device__ constexpr int few_stride(int H) { return ((H + 31) / 32 | 1) * 64; }
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(0u), "r"(a2), "r"(0u), "r"(b0), "r"(b1));
+}
+
+__global__ void __launch_bounds__(FEW_WARPS * 32) ce_few_fwd_k(const bf16* __restrict__ h, const bf16* __restrict__ W,
+                                                              const int32_t* __restrict__ target, int T, int H, int V,
+                                                              int ldz, float* __restrict__ z,
+                                                              float2* __restrict__ stat, float* __restrict__ zt) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 red[FEW_WARPS][FEW_T];
+  dep_launch();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, c = lane & 3;  // token (and row of W) and quarter of the mma's fragments
+  const int stride = few_stride(H), hv = H / 8;
+  for (int i = tid; i < FEW_T * (stride / 16); i += FEW_WARPS * 32) {
+    const int t = i / (stride / 16), v = i % (stride / 16);
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (t < T && v < hv) q = reinterpret_cast<const uint4*>(h + (int64_t)t * H)[v];
+    *reinterpret_cast<uint4*>(smem + t * stride + v * 16) = q;
+  }
+  __syncthreads();
+  const int tgt = g < T ? target[g] : -1;
+  float m = -INFINITY, s = 0.f;
+  for (int v0 = (blockIdx.x * FEW_WARPS + warp) * 16; v0 < V; v0 += gridDim.x * FEW_ROWS) {
+    // rows past the end repeat the last one; their results are dropped
+    const uint4* w0 = reinterpret_cast<const uint4*>(W + (int64_t)min(v0 + g, V - 1) * H);
+    const uint4* w1 = reinterpret_cast<const uint4*>(W + (int64_t)min(v0 + 8 + g, V - 1) * H);
+    float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    // a lane takes 8 consecutive columns of every 32: two k steps of 16, the
+    // same columns of h and W in the same lane's fragments
+    for (int k = c; k - c < hv; k += 16) {  // 16-byte vectors; up to 4 groups of 32 columns at a time
+      uint4 b0[4], b1[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        b0[u] = b1[u] = make_uint4(0, 0, 0, 0);
+        if (k + 4 * u < hv) {
+          b0[u] = __ldcs(w0 + k + 4 * u);
+          b1[u] = __ldcs(w1 + k + 4 * u);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (k - c + 4 * u >= hv) break;  // warp-uniform
+        const uint4 a = *reinterpret_cast<const uint4*>(smem + g * stride + (k + 4 * u) * 16);
+        mma_bf16(acc[0], a.x, a.y, b0[u].x, b0[u].y);
+        mma_bf16(acc[1], a.x, a.y, b1[u].x, b1[u].y);
+        mma_bf16(acc[0], a.z, a.w, b0[u].z, b0[u].w);
+        mma_bf16(acc[1], a.z, a.w, b1[u].z, b1[u].w);
+      }
+    }
+    if (g < T) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int v = v0 + 8 * j + 2 * c;
+        const float x0 = acc[j][0], x1 = acc[j][1];
+        if (z && v < V) *reinterpret_cast<float2*>(z + (int64_t)g * ldz + v) = make_float2(x0, x1);  // ldz > V, even
+        const float y0 = v < V ? x0 : -INFINITY, y1 = v + 1 < V ? x1 : -INFINITY;
+        const float mn = fmaxf(m, fmaxf(y0, y1));
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        s *= m == -INFINITY ? 1.f : ex2((m - ref) * kLog2e);
+        m = mn;
+        if (v == tgt || v + 1 == tgt) zt[g] = v == tgt ? x0 : x1;
+        s += v < V && v != tgt ? ex2((y0 - ref) * kLog2e) : 0.f;
+        s += v + 1 < V && v + 1 != tgt ? ex2((y1 - ref) * kLog2e) : 0.f;
+      }
+    }
+  }
+  auto join = [](float& m, float& s, float m2, float s2) {
+    const float M = fmaxf(m, m2);
+    if (M != -INFINITY) {
+      s = s * (m == -INFINITY ? 1.f : ex2((m - M) * kLog2e)) + s2 * (m2 == -INFINITY ? 1.f : ex2((m2 - M) * kLog2e));
+    } else {
+      s += s2;
+    }
+    m = M;
+  };
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    // the same order in both lanes, so that they hold the same bits
+    if (lane & o) {
+      float a = m2, b = s2;
+      join(a, b, m, s);
+      m = a;
+      s = b;
+    } else {
+      join(m, s, m2, s2);
+    }
+  }
+  if (c == 0) red[warp][g] = make_float2(m, s);
+  __syncthreads();
+  if (tid < T) {
+    float2 r = red[0][tid];
+    for (int w = 1; w < FEW_WARPS; ++w) join(r.x, r.y, red[w][tid].x, red[w][tid].y);
+    stat[(int64_t)tid * gridDim.x + blockIdx.x] = r;
+  }
+}
+
+constexpr int FEW_THREADS = 128, FEW_COLS = FEW_THREADS * 4;
+constexpr int FEW_STAGES = 4, FEW_SUB = 16;              // rows of W in a stage of the ring
+constexpr int FEW_STAGE = FEW_SUB * (FEW_COLS * 2 + FEW_T * 4);  // a stage: W [16][512] BF16, then z [8][16] FP32
+
+// TT: T up to 2, 4, 6 or 8.  Block (x, y): rows [x per, (x + 1) per) of W, columns
+// [512 y, 512 (y + 1)).  W and z come through a ring of bulk copies: loads of a
+// few rows ahead kept 3 of the 7 TB/s busy.
+template <int TT>
+__global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __restrict__ h, const bf16* __restrict__ W,
+                                                              const int32_t* __restrict__ target, int T, int H, int V,
+                                                              int ldz, const float* __restrict__ z,
+                                                              const float2* __restrict__ stat, int npieces,
+                                                              const float* __restrict__ zt, int per, float scale,
+                                                              float* __restrict__ row_loss, float* __restrict__ slabs,
+                                                              bf16* __restrict__ dW) {
+  extern __shared__ __align__(128) uint8_t smem[];  // [FEW_STAGES][FEW_STAGE]
+  __shared__ __align__(16) float ds[2][FEW_SUB][TT];
+  __shared__ float sM[TT], sI[TT], sD[TT];  // maximum, 1 / S (0: no target), p - 1 at the target
+  __shared__ int sT[TT];
+  __shared__ uint64_t full[FEW_STAGES];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int col0 = blockIdx.y * FEW_COLS, col = col0 + tid * 4;
+  const bool on = col < H;
+  const int r0 = blockIdx.x * per, r1 = min(V, r0 + per), stages = (r1 - r0 + FEW_SUB - 1) / FEW_SUB;
+  bool failed = false;
+  dep_launch();
+  if (tid == 0) {
+    for (int i = 0; i < FEW_STAGES; ++i) mbar_init(&full[i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  f32x2 hp[TT / 2][4], dh[TT / 2][4];
+#pragma unroll
+  for (int p = 0; p < TT / 2; ++p) {
+    uint2 a = make_uint2(0, 0), b = a;
+    if (on && 2 * p < T) a = *reinterpret_cast<const uint2*>(h + (int64_t)(2 * p) * H + col);
+    if (on && 2 * p + 1 < T) b = *reinterpret_cast<const uint2*>(h + (int64_t)(2 * p + 1) * H + col);
+    const uint32_t x[2] = {a.x, a.y}, y[2] = {b.x, b.y};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      hp[p][2 * k] = pair2(__uint_as_float(x[k] << 16), __uint_as_float(y[k] << 16));
+      hp[p][2 * k + 1] = pair2(__uint_as_float(x[k] & 0xffff0000u), __uint_as_float(y[k] & 0xffff0000u));
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dh[p][k] = 0;
+  }
+  // the first warp: stage k's rows, one a lane, and the tokens' logits of them
+  // (z's rows are padded, so that whole 64 bytes may be read past V)
+  auto fill = [&](int k) {
+    uint8_t* to = smem + (k % FEW_STAGES) * FEW_STAGE;
+    uint64_t* bar = &full[k % FEW_STAGES];
+    const int b = r0 + k * FEW_SUB, n = min(FEW_SUB, r1 - b);
+    const uint32_t bytes = (uint32_t)min(FEW_COLS, H - col0) * 2;
+    if (lane == 0) mbar_expect_tx(bar, (uint32_t)n * bytes + (uint32_t)T * FEW_SUB * 4);
+    __syncwarp();
+    if (lane < n) bulk_load(to + lane * FEW_COLS * 2, W + (int64_t)(b + lane) * H + col0, bytes, bar);
+    else if (lane >= 16 && lane - 16 < T)
+      bulk_load(to + FEW_SUB * FEW_COLS * 2 + (lane - 16) * FEW_SUB * 4, z + (int64_t)(lane - 16) * ldz + b, FEW_SUB * 4,
+                bar);
+    __syncwarp();
+  };
+  dep_wait();
+  __syncthreads();
+  if (warp == 0)
+    for (int k = 0; k < min(stages, FEW_STAGES); ++k) fill(k);
+  for (int t = warp; t < TT; t += FEW_THREADS / 32) {  // the tokens' statistics, as in ce_join_k
+    const int tgt = t < T ? target[t] : -1;
+    const bool has = tgt >= 0 && tgt < V;
+    float M = -INFINITY, rest = 0.f, S = 1.f;
+    if (has) {
+      const float2* st = stat + (int64_t)t * npieces;
+      for (int i = lane; i < npieces; i += 32) M = fmaxf(M, st[i].x);
+      M = warp_max(M);
+      for (int i = lane; i < npieces; i += 32) rest += st[i].y * (st[i].x == -INFINITY ? 1.f : expf(st[i].x - M));
+      rest = warp_sum(rest);
+      S = rest + expf(zt[t] - M);
+    }
+    if (lane == 0) {
+      sM[t] = M;
+      sI[t] = has ? 1.f / S : 0.f;
+      sD[t] = has ? -rest / S : 0.f;
+      sT[t] = has ? tgt : -1;
+      if (t < T && blockIdx.x == 0 && blockIdx.y == 0)
+        row_loss[t] = !has ? 0.f : zt[t] == M ? log1pf(rest) : (M - zt[t]) + logf(S);
+    }
+  }
+  __syncthreads();
+  for (int k = 0; k < stages; ++k) {
+    const uint8_t* st = smem + (k % FEW_STAGES) * FEW_STAGE;
+    const int b = r0 + k * FEW_SUB, n = min(FEW_SUB, r1 - b);
+    mbar_wait(&full[k % FEW_STAGES], (uint32_t)(k / FEW_STAGES) & 1, failed);
+    if (tid < TT * FEW_SUB) {  // one gradient element of the logits a thread
+      const int t = tid / FEW_SUB, r = tid % FEW_SUB;
+      float d = 0.f;
+      if (r < n && sT[t] >= 0) {
+        const float x = reinterpret_cast<const float*>(st + FEW_SUB * FEW_COLS * 2)[t * FEW_SUB + r];
+        d = b + r == sT[t] ? sD[t] : ex2((x - sM[t]) * kLog2e) * sI[t];
+      }
+      ds[k & 1][r][t] = d;
+    }
+    __syncthreads();  // also: every thread is done with the stage before, which takes a new one
+    if (warp == 0 && k >= 1 && k - 1 + FEW_STAGES < stages) fill(k - 1 + FEW_STAGES);
+    if (!on) continue;
+#pragma unroll 4
+    for (int q = 0; q < n; ++q) {
+      const uint2 w = *reinterpret_cast<const uint2*>(st + q * FEW_COLS * 2 + tid * 8);
+      f32x2 d[TT / 2];
+#pragma unroll
+      for (int p = 0; p < TT / 2; ++p) d[p] = reinterpret_cast<const f32x2*>(ds[k & 1][q])[p];
+      const uint32_t x[2] = {w.x, w.y};
+      float o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float wi = __uint_as_float(i & 1 ? x[i >> 1] & 0xffff0000u : x[i >> 1] << 16);
+        const f32x2 ww = pair2(wi, wi);
+        f32x2 a = mul2(d[0], hp[0][i]);
+#pragma unroll
+        for (int p = 1; p < TT / 2; ++p) a = fma2(d[p], hp[p][i], a);
+#pragma unroll
+        for (int p = 0; p < TT / 2; ++p) dh[p][i] = fma2(d[p], ww, dh[p][i]);
+        const float2 t = unpair2(a);
+        o[i] = (t.x + t.y) * scale;
+      }
+      if (dW) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(o[0], o[1]), hi = __floats2bfloat162_rn(o[2], o[3]);
+        *reinterpret_cast<uint2*>(dW + (int64_t)(b + q) * H + col) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      }
+    }
+  }
+  if (failed && tid == 0) {  // what is on its way lands before the block's memory goes
+    const long long t0 = clock64();
+    while (clock64() - t0 < kWaitCycles) {
+    }
+  }
+  if (!on || !slabs) return;
+  float* out = slabs + (int64_t)blockIdx.x * T * H + col;
+#pragma unroll
+  for (int p = 0; p < TT / 2; ++p) {
+    float2 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = unpair2(dh[p][k]);
+    if (2 * p < T) *reinterpret_cast<float4*>(out + (int64_t)(2 * p) * H) = make_float4(v[0].x, v[1].x, v[2].x, v[3].x);
+    if (2 * p + 1 < T)
+      *reinterpret_cast<float4*>(out + (int64_t)(2 * p + 1) * H) = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
+  }
+}
+
+// ------------------------------------------------------------------ distillation
+// A row of student logits z, teacher logits y at ids i:
+//   q = softmax over the filled slots of y / tau, p = softmax(z / tau),
+//   kd = sum_j q_j (log q_j - log p_{i_j}),  ce = lse(z) - z_target,
+//   dz_v = w_ce (softmax(z)_v - [v = target]) + w_kd / tau (p_v - sum_{i_j = v} q_j).
+// Bound by HBM: the statistics need the whole row before the first gradient
+// element.  A block takes one row at a time, and every n-th row: a producer
+// lane streams the row through a ring of shared memory with bulk copies, always
+// ahead of the warps that work on it, across row ends.  Where a row fits the
+// ring it stays there until its gradient is written; a longer one is fetched a
+// second time, from L2 (152 rows under work are at most 46 MB of 152064
+// columns).  The working warps take running sums of exp(z - m) around each
+// thread's maximum m at both temperatures, join them once per row, and write
+// the dense part of the gradient.  A further warp works out the teacher's
+// distribution of the next row meanwhile, and rewrites the at most K + 1
+// columns with a teacher entry or the target from their FP32 values once the
+// dense part stands, so that no element is rounded twice and an id that appears
+// in several slots gets the sum of their q, in slot order.
+constexpr int KD_MAX_K = 1024;
+constexpr int KD_U = 4;  // 16-byte vectors of a thread per chunk of the ring
+
+struct KdArgs {
+  int64_t rows;
+  int kcap;  // slots there is room for: K up to a power of two, at least 32
+  const bf16* logits;
+  const int32_t* target;
+  const float* t_val;
+  const int32_t* t_idx;
+  int V, K;
+  float tau, w_ce, w_kd;
+  float *row_ce, *row_kd;
+  bf16* dlogits;
+};
 
 template <int ID>
 __device__ __forceinline__ void named_sync(int n) {
@@ -1122,8 +1378,11 @@ struct CeScratch {
   uint16_t* E;
   float *dWacc, *slabs;
   int64_t ldE, chunk;
-  int npieces, runs;
+  int npieces, runs, per;  // per: rows of W of a backward block, few tokens
+  float* z;
+  int ldz;
 };
+bool ce_few(int64_t T, int H) { return T <= FEW_T && H <= FEW_MAX_H; }
 size_t ce_carve(int64_t T, int H, int V, bool grads, bool dW, uint8_t* base, CeScratch* w) {
   size_t off = 0;
   auto take = [&](int64_t bytes) {
@@ -1131,6 +1390,24 @@ size_t ce_carve(int64_t T, int H, int V, bool grads, bool dW, uint8_t* base, CeS
     off += (size_t)up(bytes, 256);
     return p;
   };
+  if (ce_few(T, H)) {
+    // forward blocks: what shared memory lets an SM hold, at most four; backward
+    // blocks: three per SM in all, of at least one stage of rows each
+    const int64_t smem = FEW_T * few_stride(H), fit = 200 * 1024 / smem < 4 ? 200 * 1024 / smem : 4;
+    const int64_t most = (V + FEW_ROWS - 1) / FEW_ROWS, ny = (H + FEW_COLS - 1) / FEW_COLS;
+    w->npieces = (int)(most < 152 * fit ? most : 152 * fit);
+    int64_t nx = 456 / ny > 0 ? 456 / ny : 1;
+    if (nx > (V + FEW_SUB - 1) / FEW_SUB) nx = (V + FEW_SUB - 1) / FEW_SUB;
+    w->per = (int)up((V + nx - 1) / nx, FEW_SUB);
+    w->runs = (V + w->per - 1) / w->per;
+    w->chunk = T;
+    w->ldz = (int)up(V + FEW_SUB, 64);
+    w->stat = (float2*)take(T * w->npieces * 8);
+    w->zt = (float*)take(T * 4);
+    w->z = grads ? (float*)take(T * w->ldz * 4) : nullptr;
+    w->slabs = grads ? (float*)take(w->runs * T * H * 4) : nullptr;
+    return off;
+  }
   w->chunk = ce_chunk(T, V);
   w->npieces = (V + 127) / 128;
   w->ldE = up(V, 64);
@@ -1288,6 +1565,51 @@ cudaError_t launch_distill(const KdArgs& a, cudaStream_t s) {
   return a.target && a.tau != 1.f ? launch_distill2<CW, NS, BPS, true>(a, s) : launch_distill2<CW, NS, BPS, false>(a, s);
 }
 
+template <int TT>
+cudaError_t launch_few_bwd(const bf16* h, const bf16* W, const int32_t* target, int T, int H, int V, float g,
+                           float* row_loss, bf16* dh, bf16* dW, const CeScratch& w, cudaStream_t s) {
+  constexpr int DEV = 16, smem = FEW_STAGES * FEW_STAGE;
+  static std::atomic<int> done[DEV];  // room for the ring, set once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev >= DEV || !done[dev].load(std::memory_order_acquire))) {
+    e = cudaFuncSetAttribute(ce_few_bwd_k<TT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && dev < DEV) done[dev].store(1, std::memory_order_release);
+  }
+  if (e != cudaSuccess) return e;
+  return launch(ce_few_bwd_k<TT>, dim3((unsigned)w.runs, (unsigned)((H + FEW_COLS - 1) / FEW_COLS)), FEW_THREADS, smem, 0,
+                true, s, h, W, target, T, H, V, w.ldz, (const float*)w.z, (const float2*)w.stat, w.npieces,
+                (const float*)w.zt, w.per, g, row_loss, dh ? w.slabs : nullptr, dW);
+}
+
+// Linear cross-entropy of up to eight tokens.
+cudaError_t linear_ce_few(const bf16* h, const bf16* W, const int32_t* target, int T, int H, int V, float g,
+                          float* row_loss, bf16* dh, bf16* dW, const CeScratch& w, cudaStream_t s) {
+  constexpr int DEV = 16;
+  static std::atomic<int> done[DEV];  // room for the widest h, set once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev >= DEV || !done[dev].load(std::memory_order_acquire))) {
+    e = cudaFuncSetAttribute(ce_few_fwd_k, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_T * few_stride(FEW_MAX_H));
+    if (e == cudaSuccess && dev < DEV) done[dev].store(1, std::memory_order_release);
+  }
+  if (e != cudaSuccess) return e;
+  e = launch(ce_few_fwd_k, dim3((unsigned)w.npieces), FEW_WARPS * 32, (size_t)FEW_T * few_stride(H), 0, false, s, h, W,
+             target, T, H, V, w.ldz, w.z, w.stat, w.zt);
+  if (e != cudaSuccess) return e;
+  if (!dh && !dW)
+    return launch(ce_join_k, dim3((unsigned)T), JOIN_THREADS, 0, 0, true, s, (const float2*)w.stat, w.npieces, target,
+                  (const float*)w.zt, V, row_loss, (uint16_t*)nullptr, (int64_t)0);
+  e = T <= 2   ? launch_few_bwd<2>(h, W, target, T, H, V, g, row_loss, dh, dW, w, s)
+      : T <= 4 ? launch_few_bwd<4>(h, W, target, T, H, V, g, row_loss, dh, dW, w, s)
+      : T <= 6 ? launch_few_bwd<6>(h, W, target, T, H, V, g, row_loss, dh, dW, w, s)
+               : launch_few_bwd<8>(h, W, target, T, H, V, g, row_loss, dh, dW, w, s);
+  if (e != cudaSuccess || !dh) return e;
+  const int64_t n4 = (int64_t)T * H / 4;
+  return launch(ce_add_runs_k, dim3((unsigned)((n4 + 31) / 32)), 256, 0, 0, true, s,
+                reinterpret_cast<const float4*>(w.slabs), n4, w.runs, g, reinterpret_cast<uint2*>(dh));
+}
+
 }  // namespace
 
 // ------------------------------------------------------------------ launchers
@@ -1307,6 +1629,7 @@ cudaError_t linear_cross_entropy(const bf16* h, const bf16* W, const int32_t* ta
   CeScratch w;
   if (ce_carve(T, H, V, grads, dW != nullptr, (uint8_t*)scratch, &w) > scratch_bytes) return cudaErrorInvalidValue;
   if (T == 0) return cudaSuccess;
+  if (ce_few(T, H)) return linear_ce_few(h, W, target, (int)T, H, V, g, row_loss, dh, dW, w, s);
   // tiles are drawn from a counter where some pair takes more than one
   const int64_t nt = (w.chunk + 255) / 256, nv = (V + 255) / 256, nh = (H + 255) / 256;
   const bool draw = nt * nv > 76 || nh * (nt * w.runs + nv) > 76;
@@ -1337,7 +1660,7 @@ cudaError_t linear_cross_entropy(const bf16* h, const bf16* W, const int32_t* ta
     if (e != cudaSuccess) return e;
     if (dh && w.runs > 1) {
       const int64_t n4 = (int64_t)rows * H / 4;
-      e = launch(ce_add_runs_k, dim3((unsigned)((n4 + 255) / 256)), 256, 0, 0, true, s,
+      e = launch(ce_add_runs_k, dim3((unsigned)((n4 + 31) / 32)), 256, 0, 0, true, s,
                  reinterpret_cast<const float4*>(w.slabs), n4, w.runs, g, reinterpret_cast<uint2*>(dh + c0 * H));
       if (e != cudaSuccess) return e;
     }

@@ -93,9 +93,12 @@ def check_lce(h, W, tgt, g, got):
 
 
 # one token, one column, ragged tiles and pieces in every dimension, a last piece of one column, V below a
-# 64-wide box, several 256-row tiles
+# 64-wide box, several 256-row tiles; up to eight tokens (a path of their own), with H at its limits: one group of
+# 32 columns and less, an even and an odd number of groups, wider than a block, the widest and one beyond
 @pytest.mark.parametrize("T,H,V", [(1, 8, 1), (1, 64, 257), (5, 256, 1000), (130, 72, 515), (256, 256, 1024),
-                                   (300, 264, 2050), (513, 128, 33), (1000, 520, 4099)])
+                                   (300, 264, 2050), (513, 128, 33), (1000, 520, 4099), (2, 296, 1258), (8, 24, 129),
+                                   (3, 96, 40001), (8, 520, 20000), (7, 2056, 130), (4, 12000, 300), (4, 12008, 300),
+                                   (9, 64, 600), (6, 1032, 9)])
 def test_linear_cross_entropy(T, H, V):
     h, W, tgt = lce_inputs(T, H, V, 1)
     tgt[::5] = -1
@@ -104,9 +107,10 @@ def test_linear_cross_entropy(T, H, V):
     check_lce(h, W, tgt, 1.0 / T, run_lce(h, W, tgt, 1.0 / T))
 
 
+@pytest.mark.parametrize("T", [6, 270])
 @pytest.mark.parametrize("dh,dW", [(False, False), (True, False), (False, True)])
-def test_linear_cross_entropy_parts_agree_with_the_whole(dh, dW):
-    h, W, tgt = lce_inputs(270, 192, 3000, 2)
+def test_linear_cross_entropy_parts_agree_with_the_whole(T, dh, dW):
+    h, W, tgt = lce_inputs(T, 192, 3000, 2)
     full = run_lce(h, W, tgt, 0.01)
     part = run_lce(h, W, tgt, 0.01, dh, dW)
     assert torch.equal(full[0], part[0])
@@ -124,27 +128,30 @@ def test_linear_cross_entropy_over_several_chunks():
     check_lce(h, W, tgt, 1.0 / T, run_lce(h, W, tgt, 1.0 / T))
 
 
-def test_linear_cross_entropy_without_any_target():
-    h, W, tgt = lce_inputs(70, 64, 300, 4)
+@pytest.mark.parametrize("T", [3, 70])
+def test_linear_cross_entropy_without_any_target(T):
+    h, W, tgt = lce_inputs(T, 64, 300, 4)
     tgt.fill_(-1)
     loss, dh, dW = run_lce(h, W, tgt, 1.0)
     assert float(loss.abs().max()) == 0.0 and float(dh.abs().max()) == 0.0 and float(dW.abs().max()) == 0.0
 
 
+@pytest.mark.parametrize("T", [8, 64])
 @pytest.mark.parametrize("std", [0.0, 80.0])
-def test_linear_cross_entropy_flat_and_large_logits(std):
+def test_linear_cross_entropy_flat_and_large_logits(T, std):
     """Equal logits (loss = log V) and logits of some hundreds, where BF16 logits would be off by whole units."""
-    h, W, tgt = lce_inputs(64, 128, 1500, 5, std)
+    h, W, tgt = lce_inputs(T, 128, 1500, 5, std)
     got = run_lce(h, W, tgt, 1.0)
     check_lce(h, W, tgt, 1.0, got)
     if std == 0.0:
         assert float((got[0] - np.log(1500)).abs().max()) < 1e-5
 
 
-def test_linear_cross_entropy_confident_rows_keep_their_digits():
+@pytest.mark.parametrize("T", [8, 64])
+def test_linear_cross_entropy_confident_rows_keep_their_digits(T):
     """The target's logit leads by about 14: its gradient element p - 1 is about -1e-4 or smaller, and dh is small
     and comes from it; the bound of check_lce scales with that small gradient."""
-    T, H, V = 64, 64, 700
+    H, V = 64, 700
     h, W, tgt = lce_inputs(T, H, V, 6, 0.2)
     W = W.clone()
     tgt = torch.arange(T, dtype=torch.int32, device="cuda")
@@ -154,19 +161,21 @@ def test_linear_cross_entropy_confident_rows_keep_their_digits():
     check_lce(h, W, tgt, 1.0, (loss, dh, dW))
 
 
-def test_linear_cross_entropy_not_a_number_stays_in_its_row():
-    h, W, tgt = lce_inputs(40, 64, 600, 7)
+@pytest.mark.parametrize("T", [8, 40])
+def test_linear_cross_entropy_not_a_number_stays_in_its_row(T):
+    h, W, tgt = lce_inputs(T, 64, 600, 7)
     want = run_lce(h, W, tgt, 1.0)
     bad = h.clone()
     bad[7, 3] = float("nan")
     loss, dh, _ = run_lce(bad, W, tgt, 1.0)
     assert bool(torch.isnan(loss[7])) and bool(torch.isnan(dh[7]).all())
-    keep = torch.arange(40, device="cuda") != 7
+    keep = torch.arange(T, device="cuda") != 7
     assert torch.equal(loss[keep], want[0][keep]) and torch.equal(dh[keep], want[1][keep])
 
 
-def test_linear_cross_entropy_gradient_matches_differences():
-    h, W, tgt = lce_inputs(33, 64, 500, 8)
+@pytest.mark.parametrize("T", [4, 33])
+def test_linear_cross_entropy_gradient_matches_differences(T):
+    h, W, tgt = lce_inputs(T, 64, 500, 8)
     g = gen(9)
     _, dh, dW = run_lce(h, W, tgt, 1.0)
     for x, d, f in ((h, dh, lambda t: ref.linear_cross_entropy(t, W, tgt, 1.0)[0].sum()),
@@ -177,8 +186,9 @@ def test_linear_cross_entropy_gradient_matches_differences():
         assert abs(diff - float((d.double() * a).sum())) <= 4 * HALF * float((d.double().abs() * a.abs()).sum())
 
 
-def test_linear_cross_entropy_same_bits_twice_and_on_another_stream():
-    h, W, tgt = lce_inputs(600, 256, 5000, 10)
+@pytest.mark.parametrize("T", [5, 600])
+def test_linear_cross_entropy_same_bits_twice_and_on_another_stream(T):
+    h, W, tgt = lce_inputs(T, 256, 5000, 10)
     a = run_lce(h, W, tgt, 0.5)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -188,9 +198,10 @@ def test_linear_cross_entropy_same_bits_twice_and_on_another_stream():
         assert torch.equal(x, y)
 
 
-def test_linear_cross_entropy_two_graphs_replayed_at_once():
+@pytest.mark.parametrize("T", [8, 520])
+def test_linear_cross_entropy_two_graphs_replayed_at_once(T):
     """Two captured calls with a workspace each, replayed on two streams at the same time with new inputs."""
-    T, H, V = 520, 256, 6000
+    H, V = 256, 6000
     cases, graphs = [lce_inputs(T, H, V, 20 + i) for i in range(2)], []
     static = [tuple(torch.empty_like(t) for t in c) for c in cases]
     outs = [(torch.empty(T, device="cuda"), torch.empty(T, H, dtype=BF, device="cuda"),
@@ -552,9 +563,10 @@ def test_losses_of_a_moe_decoder_head():
     gr = torch.autograd.grad(aux, (yn64, Wr64))
     rel = lambda a, b: float((a.double() - b).norm() / b.norm())
     # losses: FP32 for the targets; the teacher's see logits rounded to BF16, off by 2^-8 of up to about |z| / tau each
+    ce, kd, aux0 = ce.detach(), kd.detach(), aux.detach()
     assert abs(float(row_loss.sum()) - float(ce)) <= 1e-5 * float(ce)
     assert abs(float(row_kd.sum()) - float(kd)) <= HALF * float(kept.abs().max()) / tau * T
-    assert abs(float(loss.sum()) - float(aux)) <= 1e-5 * float(aux)
+    assert abs(float(loss.sum()) - float(aux0)) <= 1e-5 * float(aux0)
     # head gradients: logits, their gradient, the first of the two sums and the result are each rounded (2-norm: 2^-8
     # is the most any of them is off); the BF16 logits shift p by up to 2^-8 max|z| / tau
     tol = 5 * HALF + HALF * float(kept.abs().max()) / tau
