@@ -245,19 +245,20 @@ __global__ void __launch_bounds__(JOIN_THREADS) ce_join_k(const float2* __restri
   }
 }
 
-// dh = bf16(g sum over the runs of a split sum), n4 groups of four values; the
-// eight warps of a block take every eighth run, their sums join in warp order.
-__global__ void __launch_bounds__(256) ce_add_runs_k(const float4* __restrict__ slabs, int64_t n4, int runs, float g,
-                                                     uint2* __restrict__ dh) {
-  __shared__ float4 part[8][32];
+// dh = bf16(g sum over the runs of a split sum), n4 groups of four values; the 32
+// warps of a block take every 32nd run, their sums join in warp order.
+constexpr int RUN_WARPS = 32;
+__global__ void __launch_bounds__(RUN_WARPS * 32) ce_add_runs_k(const float4* __restrict__ slabs, int64_t n4, int runs,
+                                                               float g, uint2* __restrict__ dh) {
+  __shared__ float4 part[RUN_WARPS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t i = (int64_t)blockIdx.x * 32 + lane;
   dep_launch();
   dep_wait();
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (i < n4) {
-#pragma unroll 4
-    for (int r = warp; r < runs; r += 8) {
+#pragma unroll 8
+    for (int r = warp; r < runs; r += RUN_WARPS) {
       const float4 u = slabs[r * n4 + i];
       v.x += u.x;
       v.y += u.y;
@@ -268,8 +269,8 @@ __global__ void __launch_bounds__(256) ce_add_runs_k(const float4* __restrict__ 
   part[warp][lane] = v;
   __syncthreads();
   if (warp != 0 || i >= n4) return;
-#pragma unroll
-  for (int w = 1; w < 8; ++w) {
+#pragma unroll 8
+  for (int w = 1; w < min(RUN_WARPS, runs); ++w) {
     const float4 u = part[w][lane];
     v.x += u.x;
     v.y += u.y;
@@ -280,48 +281,62 @@ __global__ void __launch_bounds__(256) ce_add_runs_k(const float4* __restrict__ 
   dh[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// Up to eight tokens.  The products are then bound by reading W twice and
+// Up to sixteen tokens.  The products are then bound by reading W twice and
 // writing dW once, and their tiles' fixed costs weigh more than their work: of
-// a 256-row tile three per cent would be tokens, and one head of 448 by 93899
-// took 137 us of which the bytes need 25.  So W is streamed through registers:
-//   forward: z = h W^T by mma.sync (16 by 8 by 16, half of its rows used), one
-//   warp on 16 rows of W, h in shared memory; z goes to scratch in FP32 (8 rows
-//   at most) beside each block's (m, s) as in softmax_piece;
-//   backward: one thread per 4 columns of W; for every row it adds d_v W_v to
-//   its part of dh and writes dW_v = g sum_t d_tv h_t, tokens in pairs
-//   (fma.f32x2), d in FP32: no rounding but the outputs'.
-constexpr int FEW_T = 8, FEW_WARPS = 8, FEW_ROWS = FEW_WARPS * 16;
-constexpr int FEW_MAX_H = 12000;  // h in shared memory: 8 rows of up to 24 KB
+// a 256-row tile a few per cent would be tokens, and one token on a head of 448
+// by 93899 took 137 us of which the bytes need 25 (now 58).  So W is streamed
+// through registers:
+//   forward: z = h W^T by mma.sync (16 by 8 by 16; up to eight tokens leave half
+//   of its rows empty), one warp on 16 rows of W, h in shared memory; z goes to
+//   scratch in FP32 (16 rows at most) beside each block's (m, s) as in the
+//   softmax epilogue;
+//   backward: W comes through a ring of bulk copies, 16 rows by 512 columns a
+//   stage; dh += d W and dW = g d^T h by the same mma, d in BF16 as the tiles
+//   take it (with fma in FP32 it was bound by issue slots: 412 us against 160
+//   for the forward with 11 tokens).
+constexpr int FEW_T = 16, FEW_WARPS = 8, FEW_ROWS = FEW_WARPS * 16;
+constexpr int FEW_SMEM = 200 * 1024;  // the most that h may take in shared memory
 // bytes of a row of h in shared memory: whole 64-byte groups, an odd number of
 // them, so that the rows an LDS.128 touches at once lie in different banks
 __host__ __device__ constexpr int few_stride(int H) { return ((H + 31) / 32 | 1) * 64; }
+__host__ __device__ constexpr int few_held(int T) { return T <= 8 ? 8 : 16; }  // rows of h held
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(0u), "r"(a2), "r"(0u), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// HELD: 8 or 16 rows of h.
+template <int HELD>
 __global__ void __launch_bounds__(FEW_WARPS * 32) ce_few_fwd_k(const bf16* __restrict__ h, const bf16* __restrict__ W,
                                                               const int32_t* __restrict__ target, int T, int H, int V,
                                                               int ldz, float* __restrict__ z,
                                                               float2* __restrict__ stat, float* __restrict__ zt) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 red[FEW_WARPS][FEW_T];
+  constexpr int NT = HELD / 8;  // tokens a lane has results of: g and g + 8
+  __shared__ float2 red[FEW_WARPS][HELD];
   dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;  // token (and row of W) and quarter of the mma's fragments
   const int stride = few_stride(H), hv = H / 8;
-  for (int i = tid; i < FEW_T * (stride / 16); i += FEW_WARPS * 32) {
+  for (int i = tid; i < HELD * (stride / 16); i += FEW_WARPS * 32) {
     const int t = i / (stride / 16), v = i % (stride / 16);
     uint4 q = make_uint4(0, 0, 0, 0);
     if (t < T && v < hv) q = reinterpret_cast<const uint4*>(h + (int64_t)t * H)[v];
     *reinterpret_cast<uint4*>(smem + t * stride + v * 16) = q;
   }
   __syncthreads();
-  const int tgt = g < T ? target[g] : -1;
-  float m = -INFINITY, s = 0.f;
+  int tgt[NT];
+  float m[NT], s[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    tgt[i] = g + 8 * i < T ? target[g + 8 * i] : -1;
+    m[i] = -INFINITY;
+    s[i] = 0.f;
+  }
   for (int v0 = (blockIdx.x * FEW_WARPS + warp) * 16; v0 < V; v0 += gridDim.x * FEW_ROWS) {
     // rows past the end repeat the last one; their results are dropped
     const uint4* w0 = reinterpret_cast<const uint4*>(W + (int64_t)min(v0 + g, V - 1) * H);
@@ -343,26 +358,31 @@ __global__ void __launch_bounds__(FEW_WARPS * 32) ce_few_fwd_k(const bf16* __res
       for (int u = 0; u < 4; ++u) {
         if (k - c + 4 * u >= hv) break;  // warp-uniform
         const uint4 a = *reinterpret_cast<const uint4*>(smem + g * stride + (k + 4 * u) * 16);
-        mma_bf16(acc[0], a.x, a.y, b0[u].x, b0[u].y);
-        mma_bf16(acc[1], a.x, a.y, b1[u].x, b1[u].y);
-        mma_bf16(acc[0], a.z, a.w, b0[u].z, b0[u].w);
-        mma_bf16(acc[1], a.z, a.w, b1[u].z, b1[u].w);
+        uint4 e = make_uint4(0, 0, 0, 0);
+        if (NT == 2) e = *reinterpret_cast<const uint4*>(smem + (g + 8) * stride + (k + 4 * u) * 16);
+        mma_bf16(acc[0], a.x, e.x, a.y, e.y, b0[u].x, b0[u].y);
+        mma_bf16(acc[1], a.x, e.x, a.y, e.y, b1[u].x, b1[u].y);
+        mma_bf16(acc[0], a.z, e.z, a.w, e.w, b0[u].z, b0[u].w);
+        mma_bf16(acc[1], a.z, e.z, a.w, e.w, b1[u].z, b1[u].w);
       }
     }
-    if (g < T) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int t = g + 8 * i;
+      if (t >= T) continue;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int v = v0 + 8 * j + 2 * c;
-        const float x0 = acc[j][0], x1 = acc[j][1];
-        if (z && v < V) *reinterpret_cast<float2*>(z + (int64_t)g * ldz + v) = make_float2(x0, x1);  // ldz > V, even
+        const float x0 = acc[j][2 * i], x1 = acc[j][2 * i + 1];
+        if (z && v < V) *reinterpret_cast<float2*>(z + (int64_t)t * ldz + v) = make_float2(x0, x1);  // ldz > V, even
         const float y0 = v < V ? x0 : -INFINITY, y1 = v + 1 < V ? x1 : -INFINITY;
-        const float mn = fmaxf(m, fmaxf(y0, y1));
+        const float mn = fmaxf(m[i], fmaxf(y0, y1));
         const float ref = mn == -INFINITY ? 0.f : mn;
-        s *= m == -INFINITY ? 1.f : ex2((m - ref) * kLog2e);
-        m = mn;
-        if (v == tgt || v + 1 == tgt) zt[g] = v == tgt ? x0 : x1;
-        s += v < V && v != tgt ? ex2((y0 - ref) * kLog2e) : 0.f;
-        s += v + 1 < V && v + 1 != tgt ? ex2((y1 - ref) * kLog2e) : 0.f;
+        s[i] *= m[i] == -INFINITY ? 1.f : ex2((m[i] - ref) * kLog2e);
+        m[i] = mn;
+        if (v == tgt[i] || v + 1 == tgt[i]) zt[t] = v == tgt[i] ? x0 : x1;
+        s[i] += v < V && v != tgt[i] ? ex2((y0 - ref) * kLog2e) : 0.f;
+        s[i] += v + 1 < V && v + 1 != tgt[i] ? ex2((y1 - ref) * kLog2e) : 0.f;
       }
     }
   }
@@ -376,19 +396,14 @@ __global__ void __launch_bounds__(FEW_WARPS * 32) ce_few_fwd_k(const bf16* __res
     m = M;
   };
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-    // the same order in both lanes, so that they hold the same bits
-    if (lane & o) {
-      float a = m2, b = s2;
-      join(a, b, m, s);
-      m = a;
-      s = b;
-    } else {
-      join(m, s, m2, s2);
+  for (int i = 0; i < NT; ++i) {
+#pragma unroll
+    for (int o = 2; o > 0; o >>= 1) {  // lane 0 of the four holds the result
+      const float m2 = __shfl_down_sync(0xffffffffu, m[i], o), s2 = __shfl_down_sync(0xffffffffu, s[i], o);
+      join(m[i], s[i], m2, s2);
     }
+    if (c == 0) red[warp][g + 8 * i] = make_float2(m[i], s[i]);
   }
-  if (c == 0) red[warp][g] = make_float2(m, s);
   __syncthreads();
   if (tid < T) {
     float2 r = red[0][tid];
@@ -397,14 +412,36 @@ __global__ void __launch_bounds__(FEW_WARPS * 32) ce_few_fwd_k(const bf16* __res
   }
 }
 
-constexpr int FEW_THREADS = 128, FEW_COLS = FEW_THREADS * 4;
-constexpr int FEW_STAGES = 4, FEW_SUB = 16;              // rows of W in a stage of the ring
-constexpr int FEW_STAGE = FEW_SUB * (FEW_COLS * 2 + FEW_T * 4);  // a stage: W [16][512] BF16, then z [8][16] FP32
+constexpr int FEW_THREADS = 128, FEW_COLS = 512, FEW_STAGES = 4;
+// Row groups of a block: the warps have 128 columns each; narrow rows leave some
+// of them free to take every second or fourth 16 rows.
+__host__ __device__ constexpr int few_groups(int H) { return H <= 128 ? 4 : H <= 256 ? 2 : 1; }
+__host__ __device__ constexpr int few_sub(int H) { return 16 * few_groups(H); }  // rows of a stage
+// bytes from row to row of W in a stage: 16 more than the columns' own, so that
+// the eight rows an ldmatrix reads lie in different banks
+__host__ __device__ constexpr int few_wrow(int H) { return FEW_COLS * 2 / few_groups(H) + 16; }
+// A stage: rows of W in BF16, then the tokens' z of these rows in FP32.
+__host__ __device__ constexpr int few_stage(int T, int H) {
+  return (few_sub(H) * few_wrow(H) + T * few_sub(H) * 4 + 127) / 128 * 128;
+}
+// After the ring, for two stages in turn: d in BF16, [rows][16 tokens] and [16 tokens][rows].
+__host__ __device__ constexpr int few_d_bytes(int H) { return few_sub(H) * 16 * 2; }
+__host__ __device__ constexpr int few_smem(int T, int H) { return FEW_STAGES * few_stage(T, H) + 4 * few_d_bytes(H); }
 
-// TT: T up to 2, 4, 6 or 8.  Block (x, y): rows [x per, (x + 1) per) of W, columns
-// [512 y, 512 (y + 1)).  W and z come through a ring of bulk copies: loads of a
-// few rows ahead kept 3 of the 7 TB/s busy.
-template <int TT>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(su32(p))
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(su32(p))
+               : "memory");
+}
+
+// Block (x, y): rows [x per, (x + 1) per) of W, columns [512 y, 512 (y + 1)).
 __global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __restrict__ h, const bf16* __restrict__ W,
                                                               const int32_t* __restrict__ target, int T, int H, int V,
                                                               int ldz, const float* __restrict__ z,
@@ -412,65 +449,80 @@ __global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __res
                                                               const float* __restrict__ zt, int per, float scale,
                                                               float* __restrict__ row_loss, float* __restrict__ slabs,
                                                               bf16* __restrict__ dW) {
-  extern __shared__ __align__(128) uint8_t smem[];  // [FEW_STAGES][FEW_STAGE]
-  __shared__ __align__(16) float ds[2][FEW_SUB][TT];
-  __shared__ float sM[TT], sI[TT], sD[TT];  // maximum, 1 / S (0: no target), p - 1 at the target
-  __shared__ int sT[TT];
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float sM[FEW_T], sI[FEW_T], sD[FEW_T];  // maximum, 1 / S (0: no target), p - 1 at the target
+  __shared__ int sT[FEW_T];
   __shared__ uint64_t full[FEW_STAGES];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int col0 = blockIdx.y * FEW_COLS, col = col0 + tid * 4;
-  const bool on = col < H;
-  const int r0 = blockIdx.x * per, r1 = min(V, r0 + per), stages = (r1 - r0 + FEW_SUB - 1) / FEW_SUB;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int RG = few_groups(H), SUB = few_sub(H), WROW = few_wrow(H), STAGE = few_stage(T, H);
+  const int rg = warp / (4 / RG);  // this warp's row group
+  const int col0 = blockIdx.y * FEW_COLS, wcol = warp % (4 / RG) * 128, base = col0 + wcol;
+  const int ncol = min(128, H - base);  // this warp's columns: a multiple of 8, or none
+  const int r0 = blockIdx.x * per, r1 = min(V, r0 + per), stages = (r1 - r0 + SUB - 1) / SUB;
+  uint8_t* dbuf = smem + FEW_STAGES * STAGE;
   bool failed = false;
   dep_launch();
   if (tid == 0) {
     for (int i = 0; i < FEW_STAGES; ++i) mbar_init(&full[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  f32x2 hp[TT / 2][4], dh[TT / 2][4];
+  // h as the second factor of dW: tile (G, j) holds columns 32 G + 8 (n / 2) + 2 j +
+  // n % 2 for n = 0 .. 7, so that a lane's results of tiles j = 0 .. 3 are eight
+  // neighbouring columns
+  uint32_t hb[16][2];
+  const uint16_t* h16 = reinterpret_cast<const uint16_t*>(h);
 #pragma unroll
-  for (int p = 0; p < TT / 2; ++p) {
-    uint2 a = make_uint2(0, 0), b = a;
-    if (on && 2 * p < T) a = *reinterpret_cast<const uint2*>(h + (int64_t)(2 * p) * H + col);
-    if (on && 2 * p + 1 < T) b = *reinterpret_cast<const uint2*>(h + (int64_t)(2 * p + 1) * H + col);
-    const uint32_t x[2] = {a.x, a.y}, y[2] = {b.x, b.y};
+  for (int t = 0; t < 16; ++t) {
+    const int col = base + 32 * (t >> 2) + 8 * (g >> 1) + 2 * (t & 3) + (g & 1);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      hp[p][2 * k] = pair2(__uint_as_float(x[k] << 16), __uint_as_float(y[k] << 16));
-      hp[p][2 * k + 1] = pair2(__uint_as_float(x[k] & 0xffff0000u), __uint_as_float(y[k] & 0xffff0000u));
+      const int tok = 2 * c + 8 * k;
+      const uint32_t lo = col < H && tok < T ? h16[(int64_t)tok * H + col] : 0;
+      const uint32_t hi = col < H && tok + 1 < T ? h16[(int64_t)(tok + 1) * H + col] : 0;
+      hb[t][k] = lo | (hi << 16);
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) dh[p][k] = 0;
   }
-  // the first warp: stage k's rows, one a lane, and the tokens' logits of them
-  // (z's rows are padded, so that whole 64 bytes may be read past V)
+  float dh[16][4];
+#pragma unroll
+  for (int t = 0; t < 16; ++t) dh[t][0] = dh[t][1] = dh[t][2] = dh[t][3] = 0.f;
+  // the first warp: stage k's rows of W, and the tokens' logits of them (z's rows
+  // are padded, so that whole stages may be read past V)
   auto fill = [&](int k) {
-    uint8_t* to = smem + (k % FEW_STAGES) * FEW_STAGE;
+    uint8_t* to = smem + (k % FEW_STAGES) * STAGE;
     uint64_t* bar = &full[k % FEW_STAGES];
-    const int b = r0 + k * FEW_SUB, n = min(FEW_SUB, r1 - b);
-    const uint32_t bytes = (uint32_t)min(FEW_COLS, H - col0) * 2;
-    if (lane == 0) mbar_expect_tx(bar, (uint32_t)n * bytes + (uint32_t)T * FEW_SUB * 4);
+    const int b = r0 + k * SUB, n = min(SUB, r1 - b);
+    const uint32_t bytes = (uint32_t)min(FEW_COLS / RG, H - col0) * 2;
+    if (lane == 0) mbar_expect_tx(bar, (uint32_t)n * bytes + (uint32_t)(T * SUB) * 4);
     __syncwarp();
-    if (lane < n) bulk_load(to + lane * FEW_COLS * 2, W + (int64_t)(b + lane) * H + col0, bytes, bar);
-    else if (lane >= 16 && lane - 16 < T)
-      bulk_load(to + FEW_SUB * FEW_COLS * 2 + (lane - 16) * FEW_SUB * 4, z + (int64_t)(lane - 16) * ldz + b, FEW_SUB * 4,
-                bar);
+    for (int r = lane; r < n; r += 32) bulk_load(to + r * WROW, W + (int64_t)(b + r) * H + col0, bytes, bar);
+    if (lane < T) bulk_load(to + SUB * WROW + lane * SUB * 4, z + (int64_t)lane * ldz + b, (uint32_t)SUB * 4, bar);
     __syncwarp();
   };
   dep_wait();
   __syncthreads();
   if (warp == 0)
     for (int k = 0; k < min(stages, FEW_STAGES); ++k) fill(k);
-  for (int t = warp; t < TT; t += FEW_THREADS / 32) {  // the tokens' statistics, as in ce_join_k
+  for (int t = warp; t < FEW_T; t += FEW_THREADS / 32) {  // the tokens' statistics, as in ce_join_k
     const int tgt = t < T ? target[t] : -1;
     const bool has = tgt >= 0 && tgt < V;
     float M = -INFINITY, rest = 0.f, S = 1.f;
     if (has) {
       const float2* st = stat + (int64_t)t * npieces;
-      for (int i = lane; i < npieces; i += 32) M = fmaxf(M, st[i].x);
-      M = warp_max(M);
-      for (int i = lane; i < npieces; i += 32) rest += st[i].y * (st[i].x == -INFINITY ? 1.f : expf(st[i].x - M));
-      rest = warp_sum(rest);
+      for (int i = lane; i < npieces; i += 256) {  // eight loads at a time
+        float2 p[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) p[u] = i + 32 * u < npieces ? st[i + 32 * u] : make_float2(-INFINITY, 0.f);
+        float mn = M;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) mn = fmaxf(mn, p[u].x);
+        rest *= M == -INFINITY ? 1.f : expf(M - mn);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) rest += p[u].y * (p[u].x == -INFINITY ? 1.f : expf(p[u].x - mn));
+        M = mn;
+      }
+      const float wm = warp_max(M);
+      rest = warp_sum(rest * (M == -INFINITY ? 1.f : expf(M - wm)));
+      M = wm;
       S = rest + expf(zt[t] - M);
     }
     if (lane == 0) {
@@ -484,45 +536,63 @@ __global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __res
   }
   __syncthreads();
   for (int k = 0; k < stages; ++k) {
-    const uint8_t* st = smem + (k % FEW_STAGES) * FEW_STAGE;
-    const int b = r0 + k * FEW_SUB, n = min(FEW_SUB, r1 - b);
+    const uint8_t* st = smem + (k % FEW_STAGES) * STAGE;
+    const int b = r0 + k * SUB, n = min(SUB, r1 - b);
+    bf16* dT = reinterpret_cast<bf16*>(dbuf + (k & 1) * 2 * few_d_bytes(H));  // [SUB][16]
+    bf16* dN = dT + SUB * 16;                                                 // [16][SUB]
     mbar_wait(&full[k % FEW_STAGES], (uint32_t)(k / FEW_STAGES) & 1, failed);
-    if (tid < TT * FEW_SUB) {  // one gradient element of the logits a thread
-      const int t = tid / FEW_SUB, r = tid % FEW_SUB;
+    for (int i = tid; i < FEW_T * SUB; i += FEW_THREADS) {  // the logits' gradient
+      const int t = i / SUB, r = i % SUB;
       float d = 0.f;
       if (r < n && sT[t] >= 0) {
-        const float x = reinterpret_cast<const float*>(st + FEW_SUB * FEW_COLS * 2)[t * FEW_SUB + r];
+        const float x = reinterpret_cast<const float*>(st + SUB * WROW)[t * SUB + r];
         d = b + r == sT[t] ? sD[t] : ex2((x - sM[t]) * kLog2e) * sI[t];
       }
-      ds[k & 1][r][t] = d;
+      const bf16 v = __float2bfloat16_rn(d);
+      dT[r * 16 + t] = v;
+      dN[t * SUB + r] = v;
     }
-    __syncthreads();  // also: every thread is done with the stage before, which takes a new one
+    // rows past the last: their d is 0, but what an earlier stage left of W there
+    // may be no number
+    for (int i = n * (WROW / 16) + tid; i < SUB * (WROW / 16); i += FEW_THREADS)
+      reinterpret_cast<uint4*>(smem + (k % FEW_STAGES) * STAGE)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();  // also: every warp is done with the stage before, which takes a new one
     if (warp == 0 && k >= 1 && k - 1 + FEW_STAGES < stages) fill(k - 1 + FEW_STAGES);
-    if (!on) continue;
-#pragma unroll 4
-    for (int q = 0; q < n; ++q) {
-      const uint2 w = *reinterpret_cast<const uint2*>(st + q * FEW_COLS * 2 + tid * 8);
-      f32x2 d[TT / 2];
+    if (ncol <= 0 || rg * 16 >= n) continue;
+    uint32_t aT[4], aN[4];
+    // fragments of 16 by 16: lanes 0 .. 7 give the rows of the first 8 by 8 part, and so on
+    ldmatrix4(aT, dT + (rg * 16 + (lane & 15)) * 16 + (lane >> 4) * 8);
+    ldmatrix4(aN, dN + (lane & 15) * SUB + rg * 16 + (lane >> 4) * 8);
+    const uint8_t* wp = st + (rg * 16 + (lane & 15)) * WROW + wcol * 2 + (lane >> 4) * 16;
 #pragma unroll
-      for (int p = 0; p < TT / 2; ++p) d[p] = reinterpret_cast<const f32x2*>(ds[k & 1][q])[p];
-      const uint32_t x[2] = {w.x, w.y};
-      float o[4];
+    for (int G = 0; G < 4; ++G) {
+      if (32 * G >= ncol) break;
+      float o[4][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float wi = __uint_as_float(i & 1 ? x[i >> 1] & 0xffff0000u : x[i >> 1] << 16);
-        const f32x2 ww = pair2(wi, wi);
-        f32x2 a = mul2(d[0], hp[0][i]);
-#pragma unroll
-        for (int p = 1; p < TT / 2; ++p) a = fma2(d[p], hp[p][i], a);
-#pragma unroll
-        for (int p = 0; p < TT / 2; ++p) dh[p][i] = fma2(d[p], ww, dh[p][i]);
-        const float2 t = unpair2(a);
-        o[i] = (t.x + t.y) * scale;
+      for (int j = 0; j < 4; ++j) {
+        o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+        mma_bf16(o[j], aT[0], aT[1], aT[2], aT[3], hb[4 * G + j][0], hb[4 * G + j][1]);
       }
-      if (dW) {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(o[0], o[1]), hi = __floats2bfloat162_rn(o[2], o[3]);
-        *reinterpret_cast<uint2*>(dW + (int64_t)(b + q) * H + col) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t w[4];
+        ldmatrix4_t(w, wp + G * 64 + j * 32);
+        mma_bf16(dh[4 * G + 2 * j], aN[0], aN[1], aN[2], aN[3], w[0], w[1]);
+        mma_bf16(dh[4 * G + 2 * j + 1], aN[0], aN[1], aN[2], aN[3], w[2], w[3]);
+      }
+      if (dW && 32 * G + 8 * c < ncol) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = rg * 16 + g + 8 * i;
+          if (r >= n) continue;
+          uint32_t q[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(o[j][2 * i] * scale, o[j][2 * i + 1] * scale);
+            q[j] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          *reinterpret_cast<uint4*>(dW + (int64_t)(b + r) * H + base + 32 * G + 8 * c) = make_uint4(q[0], q[1], q[2], q[3]);
+        }
       }
     }
   }
@@ -531,16 +601,28 @@ __global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __res
     while (clock64() - t0 < kWaitCycles) {
     }
   }
-  if (!on || !slabs) return;
-  float* out = slabs + (int64_t)blockIdx.x * T * H + col;
+  if (!slabs) return;
+  if (RG > 1) {  // the row groups' parts, added in order through the ring's memory
+    float* part = reinterpret_cast<float*>(smem) + (int64_t)warp * 64 * 32 + lane;
+    __syncthreads();
+    if (rg > 0) {
 #pragma unroll
-  for (int p = 0; p < TT / 2; ++p) {
-    float2 v[4];
+      for (int t = 0; t < 64; ++t) part[t * 32] = dh[t >> 2][t & 3];
+    }
+    __syncthreads();
+    if (rg > 0) return;
+    for (int q = 1; q < RG; ++q) {
+      const float* other = part + q * (4 / RG) * 64 * 32;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = unpair2(dh[p][k]);
-    if (2 * p < T) *reinterpret_cast<float4*>(out + (int64_t)(2 * p) * H) = make_float4(v[0].x, v[1].x, v[2].x, v[3].x);
-    if (2 * p + 1 < T)
-      *reinterpret_cast<float4*>(out + (int64_t)(2 * p + 1) * H) = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
+      for (int t = 0; t < 64; ++t) dh[t >> 2][t & 3] += other[t * 32];
+    }
+  }
+  float* out = slabs + (int64_t)blockIdx.x * T * H + base;
+#pragma unroll
+  for (int t = 0; t < 16; ++t) {
+    if (8 * t >= ncol) break;
+    if (g < T) *reinterpret_cast<float2*>(out + (int64_t)g * H + 8 * t + 2 * c) = make_float2(dh[t][0], dh[t][1]);
+    if (g + 8 < T) *reinterpret_cast<float2*>(out + (int64_t)(g + 8) * H + 8 * t + 2 * c) = make_float2(dh[t][2], dh[t][3]);
   }
 }
 
@@ -1382,7 +1464,7 @@ struct CeScratch {
   float* z;
   int ldz;
 };
-bool ce_few(int64_t T, int H) { return T <= FEW_T && H <= FEW_MAX_H; }
+bool ce_few(int64_t T, int H) { return T <= FEW_T && (int64_t)few_held((int)T) * few_stride(H) <= FEW_SMEM; }
 size_t ce_carve(int64_t T, int H, int V, bool grads, bool dW, uint8_t* base, CeScratch* w) {
   size_t off = 0;
   auto take = [&](int64_t bytes) {
@@ -1392,16 +1474,19 @@ size_t ce_carve(int64_t T, int H, int V, bool grads, bool dW, uint8_t* base, CeS
   };
   if (ce_few(T, H)) {
     // forward blocks: what shared memory lets an SM hold, at most four; backward
-    // blocks: three per SM in all, of at least one stage of rows each
-    const int64_t smem = FEW_T * few_stride(H), fit = 200 * 1024 / smem < 4 ? 200 * 1024 / smem : 4;
+    // blocks: the two or three per SM that run at once, of at least one stage of
+    // rows each
+    const int64_t smem = few_held((int)T) * few_stride(H), fit = FEW_SMEM / smem < 4 ? FEW_SMEM / smem : 4;
+    const int sub = few_sub(H);
     const int64_t most = (V + FEW_ROWS - 1) / FEW_ROWS, ny = (H + FEW_COLS - 1) / FEW_COLS;
     w->npieces = (int)(most < 152 * fit ? most : 152 * fit);
-    int64_t nx = 456 / ny > 0 ? 456 / ny : 1;
-    if (nx > (V + FEW_SUB - 1) / FEW_SUB) nx = (V + FEW_SUB - 1) / FEW_SUB;
-    w->per = (int)up((V + nx - 1) / nx, FEW_SUB);
+    const int64_t bps = 226 * 1024 / (few_smem((int)T, H) + 1024) < 3 ? 2 : 3;
+    int64_t nx = 152 * bps / ny > 0 ? 152 * bps / ny : 1;
+    if (nx > (V + sub - 1) / sub) nx = (V + sub - 1) / sub;
+    w->per = (int)up((V + nx - 1) / nx, sub);
     w->runs = (V + w->per - 1) / w->per;
     w->chunk = T;
-    w->ldz = (int)up(V + FEW_SUB, 64);
+    w->ldz = (int)up(V + sub, 64);
     w->stat = (float2*)take(T * w->npieces * 8);
     w->zt = (float*)take(T * 4);
     w->z = grads ? (float*)take(T * w->ldz * 4) : nullptr;
@@ -1565,48 +1650,51 @@ cudaError_t launch_distill(const KdArgs& a, cudaStream_t s) {
   return a.target && a.tau != 1.f ? launch_distill2<CW, NS, BPS, true>(a, s) : launch_distill2<CW, NS, BPS, false>(a, s);
 }
 
-template <int TT>
 cudaError_t launch_few_bwd(const bf16* h, const bf16* W, const int32_t* target, int T, int H, int V, float g,
                            float* row_loss, bf16* dh, bf16* dW, const CeScratch& w, cudaStream_t s) {
-  constexpr int DEV = 16, smem = FEW_STAGES * FEW_STAGE;
-  static std::atomic<int> done[DEV];  // room for the ring, set once per device
+  constexpr int DEV = 16, most = few_smem(FEW_T, 8) > few_smem(FEW_T, 512) ? few_smem(FEW_T, 8) : few_smem(FEW_T, 512);
+  static std::atomic<int> done[DEV];  // room for the largest ring, set once per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && (dev >= DEV || !done[dev].load(std::memory_order_acquire))) {
-    e = cudaFuncSetAttribute(ce_few_bwd_k<TT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(ce_few_bwd_k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e == cudaSuccess && dev < DEV) done[dev].store(1, std::memory_order_release);
   }
   if (e != cudaSuccess) return e;
-  return launch(ce_few_bwd_k<TT>, dim3((unsigned)w.runs, (unsigned)((H + FEW_COLS - 1) / FEW_COLS)), FEW_THREADS, smem, 0,
-                true, s, h, W, target, T, H, V, w.ldz, (const float*)w.z, (const float2*)w.stat, w.npieces,
-                (const float*)w.zt, w.per, g, row_loss, dh ? w.slabs : nullptr, dW);
+  return launch(ce_few_bwd_k, dim3((unsigned)w.runs, (unsigned)((H + FEW_COLS - 1) / FEW_COLS)),
+                FEW_THREADS, (size_t)few_smem(T, H), 0, true, s, h, W, target, T, H, V, w.ldz, (const float*)w.z,
+                (const float2*)w.stat, w.npieces, (const float*)w.zt, w.per, g, row_loss, dh ? w.slabs : nullptr, dW);
 }
 
-// Linear cross-entropy of up to eight tokens.
-cudaError_t linear_ce_few(const bf16* h, const bf16* W, const int32_t* target, int T, int H, int V, float g,
-                          float* row_loss, bf16* dh, bf16* dW, const CeScratch& w, cudaStream_t s) {
+template <int HELD>
+cudaError_t launch_few_fwd(const bf16* h, const bf16* W, const int32_t* target, int T, int H, int V, const CeScratch& w,
+                           cudaStream_t s) {
   constexpr int DEV = 16;
   static std::atomic<int> done[DEV];  // room for the widest h, set once per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && (dev >= DEV || !done[dev].load(std::memory_order_acquire))) {
-    e = cudaFuncSetAttribute(ce_few_fwd_k, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_T * few_stride(FEW_MAX_H));
+    e = cudaFuncSetAttribute(ce_few_fwd_k<HELD>, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM);
     if (e == cudaSuccess && dev < DEV) done[dev].store(1, std::memory_order_release);
   }
   if (e != cudaSuccess) return e;
-  e = launch(ce_few_fwd_k, dim3((unsigned)w.npieces), FEW_WARPS * 32, (size_t)FEW_T * few_stride(H), 0, false, s, h, W,
-             target, T, H, V, w.ldz, w.z, w.stat, w.zt);
+  return launch(ce_few_fwd_k<HELD>, dim3((unsigned)w.npieces), FEW_WARPS * 32, (size_t)HELD * few_stride(H), 0, false, s,
+                h, W, target, T, H, V, w.ldz, w.z, w.stat, w.zt);
+}
+
+// Linear cross-entropy of up to sixteen tokens.
+cudaError_t linear_ce_few(const bf16* h, const bf16* W, const int32_t* target, int T, int H, int V, float g,
+                          float* row_loss, bf16* dh, bf16* dW, const CeScratch& w, cudaStream_t s) {
+  cudaError_t e = few_held(T) == 8 ? launch_few_fwd<8>(h, W, target, T, H, V, w, s)
+                                   : launch_few_fwd<16>(h, W, target, T, H, V, w, s);
   if (e != cudaSuccess) return e;
   if (!dh && !dW)
     return launch(ce_join_k, dim3((unsigned)T), JOIN_THREADS, 0, 0, true, s, (const float2*)w.stat, w.npieces, target,
                   (const float*)w.zt, V, row_loss, (uint16_t*)nullptr, (int64_t)0);
-  e = T <= 2   ? launch_few_bwd<2>(h, W, target, T, H, V, g, row_loss, dh, dW, w, s)
-      : T <= 4 ? launch_few_bwd<4>(h, W, target, T, H, V, g, row_loss, dh, dW, w, s)
-      : T <= 6 ? launch_few_bwd<6>(h, W, target, T, H, V, g, row_loss, dh, dW, w, s)
-               : launch_few_bwd<8>(h, W, target, T, H, V, g, row_loss, dh, dW, w, s);
+  e = launch_few_bwd(h, W, target, T, H, V, g, row_loss, dh, dW, w, s);
   if (e != cudaSuccess || !dh) return e;
   const int64_t n4 = (int64_t)T * H / 4;
-  return launch(ce_add_runs_k, dim3((unsigned)((n4 + 31) / 32)), 256, 0, 0, true, s,
+  return launch(ce_add_runs_k, dim3((unsigned)((n4 + 31) / 32)), RUN_WARPS * 32, 0, 0, true, s,
                 reinterpret_cast<const float4*>(w.slabs), n4, w.runs, g, reinterpret_cast<uint2*>(dh));
 }
 
@@ -1660,7 +1748,7 @@ cudaError_t linear_cross_entropy(const bf16* h, const bf16* W, const int32_t* ta
     if (e != cudaSuccess) return e;
     if (dh && w.runs > 1) {
       const int64_t n4 = (int64_t)rows * H / 4;
-      e = launch(ce_add_runs_k, dim3((unsigned)((n4 + 31) / 32)), 256, 0, 0, true, s,
+      e = launch(ce_add_runs_k, dim3((unsigned)((n4 + 31) / 32)), RUN_WARPS * 32, 0, 0, true, s,
                  reinterpret_cast<const float4*>(w.slabs), n4, w.runs, g, reinterpret_cast<uint2*>(dh + c0 * H));
       if (e != cudaSuccess) return e;
     }
@@ -1678,16 +1766,27 @@ cudaError_t distill_topk(const bf16* logits, const int32_t* target, const float*
   int kcap = 32;
   while (kcap < K) kcap *= 2;
   const KdArgs a{rows, kcap, logits, target, t_val, t_idx, V, K, tau, w_ce, w_kd, row_ce, row_kd, dlogits};
-  // working warps by the row's length, each rule with both sides measured (us,
-  // GB300): one warp and 12 blocks per SM up to 12288 columns (8192 rows of
-  // 12288: 88 against 95 with four warps; of 16384: 125 against 102); four warps
-  // up to 24576 (of 24576: 157 against 183 with eight; of 28000: 177 against
-  // 170); eight up to 65536 (4096 rows of 64000: 196 against 209 with sixteen;
-  // of 80000: 252 against 214, where two rows per SM no longer stay in L2 until
-  // they are read again)
-  if (V <= 12288) return launch_distill<1, 6, 12>(a, s);
-  if (V <= 24576) return launch_distill<4, 6, 4>(a, s);
-  if (V <= 65536) return launch_distill<8, 6, 2>(a, s);
+  // working warps of a block, by the row's length and the number of rows; each
+  // rule with both sides measured (us, GB300)
+  //   many rows: one warp and 12 blocks per SM up to 12288 columns (8192 rows of
+  //   12288: 88 against 95 with four warps; of 16384: 125 against 102), four up
+  //   to 24576 (of 24576: 157 against 183 with eight; of 28000: 177 against 170),
+  //   eight up to 65536 (4096 rows of 64000: 196 against 209 with sixteen; of
+  //   80000: 252 against 214, where two rows per SM no longer stay in L2 until
+  //   they are read again)
+  int warps = V <= 12288 ? 1 : V <= 24576 ? 4 : V <= 65536 ? 8 : 16;
+  //   few rows, so that a row's own time counts: four warps while their 608
+  //   blocks take all rows at once (304 rows of 4096: 4.6 against 6.7 with one;
+  //   600: 7.8 against 9.2; 1200: 11.4 against 10.4), with long rows for four
+  //   times as many (2400 rows of 8192: 22.6 against 28.2); eight while 304 do
+  //   (152 rows of 24000: 6.0 against 7.0 with four), sixteen while 152 do (152
+  //   rows of 48000: 8.2 against 8.8 with eight)
+  if (V > 2048 && warps < 4 && (rows <= 608 || (V >= 8192 && rows <= 2432))) warps = 4;
+  if (V > 16384 && warps < 8 && rows <= 304) warps = 8;
+  if (V > 32768 && rows <= 152) warps = 16;
+  if (warps == 1) return launch_distill<1, 6, 12>(a, s);
+  if (warps == 4) return launch_distill<4, 6, 4>(a, s);
+  if (warps == 8) return launch_distill<8, 6, 2>(a, s);
   return launch_distill<16, 5, 1>(a, s);
 }
 

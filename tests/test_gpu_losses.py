@@ -93,12 +93,13 @@ def check_lce(h, W, tgt, g, got):
 
 
 # one token, one column, ragged tiles and pieces in every dimension, a last piece of one column, V below a
-# 64-wide box, several 256-row tiles; up to eight tokens (a path of their own), with H at its limits: one group of
+# 64-wide box, several 256-row tiles; up to sixteen tokens (a path of their own), with H at its limits: one group of
 # 32 columns and less, an even and an odd number of groups, wider than a block, the widest and one beyond
 @pytest.mark.parametrize("T,H,V", [(1, 8, 1), (1, 64, 257), (5, 256, 1000), (130, 72, 515), (256, 256, 1024),
                                    (300, 264, 2050), (513, 128, 33), (1000, 520, 4099), (2, 296, 1258), (8, 24, 129),
-                                   (3, 96, 40001), (8, 520, 20000), (7, 2056, 130), (4, 12000, 300), (4, 12008, 300),
-                                   (9, 64, 600), (6, 1032, 9)])
+                                   (3, 96, 40001), (8, 520, 20000), (7, 2056, 130), (4, 12768, 300), (4, 12776, 300),
+                                   (9, 64, 600), (6, 1032, 9), (16, 6368, 200), (16, 6400, 200), (15, 256, 5000),
+                                   (16, 136, 3001), (11, 520, 9000), (10, 64, 1), (17, 64, 700), (12, 40, 4111)])
 def test_linear_cross_entropy(T, H, V):
     h, W, tgt = lce_inputs(T, H, V, 1)
     tgt[::5] = -1
