@@ -1254,18 +1254,9 @@ void init_once() {
                                 (const void*)gemm_pair_kernel<1, false, true, false, false, 2>,
                                 (const void*)gemm_pair_kernel<1, true, false, false, false, 2>,
                                 (const void*)gemm_pair_kernel<1, true, true, false, false, 2>,
-                                (const void*)gemm_pair_kernel<2, true, true, false, true, 2>,
-                                (const void*)gemm_pair_kernel<1, false, false, false, false, 1, 1>};
+                                (const void*)gemm_pair_kernel<2, true, true, false, true, 2>};
   for (const void* k : pair_kernels) {
     const cudaError_t a = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM_BYTES);
-    if (a != cudaSuccess) g_init_err = a;
-  }
-  const void* loss_kernels[] = {(const void*)gemm_pair_kernel<1, false, false, false, false, 1, 2>,
-                                (const void*)gemm_pair_kernel<2, false, true, true, true, 1, 3>,
-                                (const void*)gemm_pair_kernel<1, false, true, false, false, 1, 3>,
-                                (const void*)gemm_pair_kernel<1, true, true, false, false, 1, 3>};
-  for (const void* k : loss_kernels) {
-    const cudaError_t a = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, p_smem<3>());
     if (a != cudaSuccess) g_init_err = a;
   }
   // pairs resident at once (an SM pair shares a TPC; the count can be below SMs / 2)
@@ -1561,10 +1552,36 @@ cudaError_t gemm_pair(const GemmArgs& g0, const GemmArgs& g1, cudaStream_t s) {
   return e != cudaSuccess ? e : launch(&g1, 1, s);
 }
 
-cudaError_t gemm_softmax_pieces(const bf16* A, const bf16* B, int M, int N, int K, const SoftmaxPieces& sp,
-                                int* tile_ctr, bool dependent, cudaStream_t s) {
+namespace {
+// The linear cross-entropy's kernels: their shared memory is a setting per
+// device, made at the first call on each.
+cudaError_t loss_kernels_ready() {
   std::call_once(g_once, init_once);
   if (g_init_err != cudaSuccess) return g_init_err;
+  constexpr int DEV = 16;
+  static std::atomic<int> done[DEV];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < DEV && done[dev].load(std::memory_order_acquire))) return e;
+  const struct {
+    const void* kernel;
+    int smem;
+  } all[] = {{(const void*)gemm_pair_kernel<1, false, false, false, false, 1, 1>, p_smem<1>()},
+             {(const void*)gemm_pair_kernel<1, false, false, false, false, 1, 2>, p_smem<2>()},
+             {(const void*)gemm_pair_kernel<2, false, true, true, true, 1, 3>, p_smem<3>()},
+             {(const void*)gemm_pair_kernel<1, false, true, false, false, 1, 3>, p_smem<3>()},
+             {(const void*)gemm_pair_kernel<1, true, true, false, false, 1, 3>, p_smem<3>()}};
+  for (const auto& k : all)
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+  if (e == cudaSuccess && dev < DEV) done[dev].store(1, std::memory_order_release);
+  return e;
+}
+}  // namespace
+
+cudaError_t gemm_softmax_pieces(const bf16* A, const bf16* B, int M, int N, int K, const SoftmaxPieces& sp,
+                                int* tile_ctr, bool dependent, cudaStream_t s) {
+  const cudaError_t ready = loss_kernels_ready();
+  if (ready != cudaSuccess) return ready;
   if (M <= 0 || N <= 0 || K <= 0 || K % 8 || !al16(A) || !al16(B) || !sp.stat || !sp.zt || !sp.target)
     return cudaErrorInvalidValue;
   if (sp.npieces != (N + 127) / 128 || (sp.E && (!al16(sp.E) || sp.ldE % 8 || sp.ldE < N))) return cudaErrorInvalidValue;
@@ -1586,8 +1603,8 @@ cudaError_t gemm_softmax_pieces(const bf16* A, const bf16* B, int M, int N, int 
 }
 
 cudaError_t gemm_grads(const GradArgs& g, cudaStream_t s) {
-  std::call_once(g_once, init_once);
-  if (g_init_err != cudaSuccess) return g_init_err;
+  const cudaError_t ready = loss_kernels_ready();
+  if (ready != cudaSuccess) return ready;
   if (!(g.dgrad || g.wgrad) || (g.dgrad && (g.dgrad->a_mn || !g.dgrad->b_mn)) ||
       (g.wgrad && (!g.wgrad->a_mn || !g.wgrad->b_mn)))
     return cudaErrorInvalidValue;

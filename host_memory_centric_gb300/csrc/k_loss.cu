@@ -174,15 +174,18 @@ __device__ __forceinline__ void async_load4(void* dst, const void* src) {
 // and gradient of a confident row (p near 1) keep their digits.  The factor g
 // of the gradients waits for the products' FP32 results: rounded here, g (p - 1)
 // of most rows would be off by the same amount, and the errors would add up.
-// Rows without a target get zeros.  Bound by HBM (4 bytes a logit).  The blocks
-// of grid.y share a row; each joins the statistics for itself.
+// Rows without a target get zeros, and zeros in hm too, a copy of h for dW = d^T
+// h: what padding holds may be no number, and 0 times that would not be 0.
+// Bound by HBM (4 bytes a logit).  The blocks of grid.y share a row; each joins
+// the statistics for itself.
 constexpr int JOIN_THREADS = 256;
 
 __global__ void __launch_bounds__(JOIN_THREADS) ce_join_k(const float2* __restrict__ stat, int npieces,
                                                           const int32_t* __restrict__ target,
                                                           const float* __restrict__ zt, int V,
                                                           float* __restrict__ row_loss, uint16_t* __restrict__ E,
-                                                          int64_t ldE) {
+                                                          int64_t ldE, const bf16* __restrict__ h,
+                                                          bf16* __restrict__ hm, int H) {
   __shared__ float red[JOIN_THREADS / 32];
   dep_launch();
   dep_wait();
@@ -190,6 +193,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) ce_join_k(const float2* __restri
   const int tgt = target[row];
   const bool has = tgt >= 0 && tgt < V;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (hm && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < H / 8; i += JOIN_THREADS)
+      reinterpret_cast<uint4*>(hm + row * H)[i] =
+          has ? reinterpret_cast<const uint4*>(h + row * H)[i] : make_uint4(0, 0, 0, 0);
   uint4* e = reinterpret_cast<uint4*>(E + row * ldE);
   const int nvec = (V + 7) / 8, step = 32 * (JOIN_THREADS / 32) * (int)gridDim.y;
   const int first = ((int)blockIdx.y * (JOIN_THREADS / 32) + warp) * 32 + lane;
@@ -469,16 +476,25 @@ __global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __res
   // h as the second factor of dW: tile (G, j) holds columns 32 G + 8 (n / 2) + 2 j +
   // n % 2 for n = 0 .. 7, so that a lane's results of tiles j = 0 .. 3 are eight
   // neighbouring columns
+  // (tokens without a target are left out: what padding holds may be no number)
   uint32_t hb[16][2];
   const uint16_t* h16 = reinterpret_cast<const uint16_t*>(h);
+  bool used[2][2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int tok = 2 * c + 8 * k + i, tgt = tok < T ? target[tok] : -1;
+      used[k][i] = tgt >= 0 && tgt < V;
+    }
 #pragma unroll
   for (int t = 0; t < 16; ++t) {
     const int col = base + 32 * (t >> 2) + 8 * (g >> 1) + 2 * (t & 3) + (g & 1);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int tok = 2 * c + 8 * k;
-      const uint32_t lo = col < H && tok < T ? h16[(int64_t)tok * H + col] : 0;
-      const uint32_t hi = col < H && tok + 1 < T ? h16[(int64_t)(tok + 1) * H + col] : 0;
+      const uint32_t lo = col < H && used[k][0] ? h16[(int64_t)tok * H + col] : 0;
+      const uint32_t hi = col < H && used[k][1] ? h16[(int64_t)(tok + 1) * H + col] : 0;
       hb[t][k] = lo | (hi << 16);
     }
   }
@@ -1458,6 +1474,7 @@ struct CeScratch {
   float2* stat;
   float* zt;
   uint16_t* E;
+  bf16* hm;
   float *dWacc, *slabs;
   int64_t ldE, chunk;
   int npieces, runs, per;  // per: rows of W of a backward block, few tokens
@@ -1500,6 +1517,7 @@ size_t ce_carve(int64_t T, int H, int V, bool grads, bool dW, uint8_t* base, CeS
   w->stat = (float2*)take(w->chunk * w->npieces * 8);
   w->zt = (float*)take(w->chunk * 4);
   w->E = grads ? (uint16_t*)take(w->chunk * w->ldE * 2) : nullptr;
+  w->hm = grads ? (bf16*)take(w->chunk * H * 2) : nullptr;
   w->dWacc = grads && w->chunk < T ? (float*)take((int64_t)V * H * 4) : nullptr;
   // the runs with dW beside them or without: room for the larger number
   const int a = grads ? ce_runs(w->chunk, H, V, true) : 1, b = grads ? ce_runs(w->chunk, H, V, false) : 1;
@@ -1690,7 +1708,7 @@ cudaError_t linear_ce_few(const bf16* h, const bf16* W, const int32_t* target, i
   if (e != cudaSuccess) return e;
   if (!dh && !dW)
     return launch(ce_join_k, dim3((unsigned)T), JOIN_THREADS, 0, 0, true, s, (const float2*)w.stat, w.npieces, target,
-                  (const float*)w.zt, V, row_loss, (uint16_t*)nullptr, (int64_t)0);
+                  (const float*)w.zt, V, row_loss, (uint16_t*)nullptr, (int64_t)0, (const bf16*)nullptr, (bf16*)nullptr, H);
   e = launch_few_bwd(h, W, target, T, H, V, g, row_loss, dh, dW, w, s);
   if (e != cudaSuccess || !dh) return e;
   const int64_t n4 = (int64_t)T * H / 4;
@@ -1734,12 +1752,13 @@ cudaError_t linear_cross_entropy(const bf16* h, const bf16* W, const int32_t* ta
     // few rows: several blocks share each, down to about 2048 columns a block
     const int want = 1216 / rows, most = (V + 2047) / 2048, split = want < 1 || !w.E ? 1 : want < most ? want : most;
     e = launch(ce_join_k, dim3((unsigned)rows, (unsigned)split), JOIN_THREADS, 0, 0, true, s, (const float2*)w.stat,
-               w.npieces, target + c0, (const float*)w.zt, V, row_loss + c0, w.E, w.ldE);
+               w.npieces, target + c0, (const float*)w.zt, V, row_loss + c0, w.E, w.ldE, h + c0 * H,
+               dW ? w.hm : nullptr, H);
     if (e != cudaSuccess) return e;
     if (!grads) continue;
     const bf16* d = reinterpret_cast<const bf16*>(w.E);
     const GemmArgs gd{d, w.ldE, 0, W, H, 1, rows, H, V, dh ? dh + c0 * H : nullptr, H, nullptr, 0, nullptr, 0, 0};
-    GemmArgs gw{d, w.ldE, 1, h + c0 * H, H, 1, V, H, rows, last ? dW : nullptr, H, nullptr, 0, nullptr, H, 0};
+    GemmArgs gw{d, w.ldE, 1, w.hm, H, 1, V, H, rows, last ? dW : nullptr, H, nullptr, 0, nullptr, H, 0};
     if (w.dWacc) {
       gw.Dacc = w.dWacc;
       gw.acc_mode = first ? 1 : 2;
@@ -1799,7 +1818,7 @@ size_t router_balance_scratch(int64_t T, int S, int E) {
 cudaError_t router_balance(const float* logits, const int32_t* idx, const uint8_t* valid, int64_t T, int S, int E,
                            int k, float alpha, float z_coef, float* loss, int32_t* counts, float* prob, bf16* dlogits,
                            void* scratch, size_t scratch_bytes, cudaStream_t s) {
-  if (!bal_shape_ok(T, S, E) || k < 1 || k > E || (int64_t)S * k > 0x7fffffff || !al16(logits) || !al16(dlogits) || !al16(idx) ||
+  if (!bal_shape_ok(T, S, E) || k < 1 || k > E || (int64_t)S * k > (1 << 30) || !al16(logits) || !al16(dlogits) || !al16(idx) ||
       (reinterpret_cast<uintptr_t>(scratch) & 255))
     return cudaErrorInvalidValue;
   if (T == 0) return cudaSuccess;

@@ -459,8 +459,10 @@ mt_status mt_cross_entropy(void* logits, const int32_t* target, int64_t rows, in
  * aligned device memory of
  * mt_linear_cross_entropy_scratch_bytes(T, H, V, dh or dW wanted) bytes, not
  * shared by calls that may overlap.  H a multiple of 8, V <= 2097152, h, W, dh
- * and dW 16-byte aligned, else MT_ERR_ARG.  T = 0 writes nothing.  No host
- * synchronisation; may be captured into a graph. */
+ * and dW 16-byte aligned, else MT_ERR_ARG; the outputs must not overlap the
+ * inputs.  T = 0 writes nothing.  No host synchronisation; may be captured into
+ * a graph, after the first GEMM of the process (mt_gemm, or one such call),
+ * which allocates. */
 size_t mt_linear_cross_entropy_scratch_bytes(int64_t T, int32_t H, int32_t V, int32_t grads);
 mt_status mt_linear_cross_entropy(const void* h, const void* W, const int32_t* target, int64_t T, int32_t H, int32_t V,
                                   float inv_norm, float* row_loss, void* dh, void* dW, void* scratch,
@@ -478,7 +480,8 @@ mt_status mt_linear_cross_entropy(const void* h, const void* W, const int32_t* t
  * its q.  A row with no filled slot (or none above -inf) has no teacher part,
  * a target outside [0, V) no hard part; a row with neither gets zeros.
  * row_ce may be null.  1 <= K <= 1024, tau and 1 / tau finite and > 0,
- * logits and dlogits 16-byte aligned, else MT_ERR_ARG; V may be odd. */
+ * logits and dlogits 16-byte aligned, else MT_ERR_ARG; V may be odd.  No host
+ * synchronisation; may be captured into a graph. */
 mt_status mt_distill_topk(const void* logits, const int32_t* target, const float* t_val, const int32_t* t_idx,
                           int64_t rows, int32_t V, int32_t K, float tau, float w_ce, float w_kd, float* row_ce,
                           float* row_kd, void* dlogits, void* stream);
@@ -496,9 +499,9 @@ mt_status mt_distill_topk(const void* logits, const int32_t* target, const float
  * and has zero counts and prob.  To add it to mt_moe_ffn's gradients, multiply
  * it with Wr and yn (mt_gemm).  scratch: 256-byte aligned device memory of
  * mt_router_balance_scratch_bytes(T, S, E) bytes, not shared by calls that may
- * overlap.  1 <= k <= E <= 512, S a divisor of T, at most 65535 groups, S k <
- * 2^31, logits, idx and dlogits 16-byte aligned, else MT_ERR_ARG.  T = 0
- * writes nothing. */
+ * overlap.  1 <= k <= E <= 512, S a divisor of T, at most 65535 groups, S k <=
+ * 2^30, logits, idx and dlogits 16-byte aligned, else MT_ERR_ARG.  T = 0
+ * writes nothing.  No host synchronisation; may be captured into a graph. */
 size_t mt_router_balance_scratch_bytes(int64_t T, int32_t S, int32_t E);
 mt_status mt_router_balance(const float* logits, const int32_t* idx, const uint8_t* valid, int64_t T, int32_t S,
                             int32_t E, int32_t k, float alpha, float z_coef, float* loss, int32_t* counts, float* prob,

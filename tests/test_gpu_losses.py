@@ -174,6 +174,19 @@ def test_linear_cross_entropy_not_a_number_stays_in_its_row(T):
     assert torch.equal(loss[keep], want[0][keep]) and torch.equal(dh[keep], want[1][keep])
 
 
+@pytest.mark.parametrize("T", [8, 40])
+def test_linear_cross_entropy_padding_may_hold_anything(T):
+    """Rows without a target hold NaN and infinities: they leave no trace in any output."""
+    h, W, tgt = lce_inputs(T, 64, 600, 17)
+    tgt[1::3] = -1
+    clean = h.clone()
+    clean[1::3] = 0
+    h[1::3, ::2] = float("nan")
+    h[4] = float("inf")
+    for a, b in zip(run_lce(h, W, tgt, 0.5), run_lce(clean, W, tgt, 0.5)):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("T", [4, 33])
 def test_linear_cross_entropy_gradient_matches_differences(T):
     h, W, tgt = lce_inputs(T, 64, 500, 8)
@@ -230,6 +243,18 @@ def test_linear_cross_entropy_two_graphs_replayed_at_once(T):
     for i in range(2):
         for x, y in zip(outs[i], want[i]):
             assert torch.equal(x, y)
+
+
+def test_linear_cross_entropy_reports_a_wait_that_ran_out():
+    """A product that gets no operands (injected on the host) ends by itself and is reported; the next call is right."""
+    h, W, tgt = lce_inputs(300, 64, 700, 30)
+    want = run_lce(h, W, tgt, 1.0)
+    for nth in (1, 2):  # the logits' product, then the gradients' too
+        mt.lib().mt_fault_inject(4, nth)
+        run_lce(h, W, tgt, 1.0)
+        assert ops.kernel_error(clear=True) != 0
+        for a, b in zip(run_lce(h, W, tgt, 1.0), want):
+            assert torch.equal(a, b)
 
 
 # ------------------------------------------------------------------ distillation
@@ -297,9 +322,16 @@ def test_distill_missing_slots_targets_and_rows():
     ids[8] = ids[8, 0]      # the same id in every slot
     ids[9, 0] = int(tgt[9]) if 0 <= int(tgt[9]) < V else 0
     tgt[10] = ids[10, 2]
-    got = run_kd(z, tgt, y, ids, 1.5, 0.5, 1.0)
-    check_kd(z, tgt, y, ids, 1.5, 0.5, 1.0, got)
     none = ((tgt < 0) | (tgt >= V)) & (((ids < 0) | (ids >= V)).all(1) | (y == -float("inf")).all(1))
+    z[none] = 0
+    want = run_kd(z, tgt, y, ids, 1.5, 0.5, 1.0)
+    check_kd(z, tgt, y, ids, 1.5, 0.5, 1.0, want)
+    # padding may hold anything, and so may empty slots
+    z[none] = float("nan")
+    y[(ids < 0) | (ids >= V)] = float("nan")
+    got = run_kd(z, tgt, y, ids, 1.5, 0.5, 1.0)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
     assert bool(none.any())
     assert float(got[2][none].abs().max()) == 0.0 and float(got[1][none].abs().max()) == 0.0
 

@@ -58,7 +58,7 @@ def bal(logits=P, idx=P, valid=P, T=32, S=8, E=16, k=2, loss=P, counts=P, prob=P
 @pytest.mark.parametrize("bad", [dict(logits=None), dict(idx=None), dict(loss=None), dict(counts=None),
                                  dict(prob=None), dict(scratch=None), dict(T=33), dict(S=0), dict(S=-8), dict(T=-8),
                                  dict(E=0), dict(E=513), dict(k=0), dict(k=17), dict(T=1 << 20, S=8),
-                                 dict(T=1 << 30, S=1 << 30, k=4), dict(logits=P + 4), dict(dlogits=P + 2),
+                                 dict(T=1 << 30, S=1 << 30, k=2), dict(logits=P + 4), dict(dlogits=P + 2),
                                  dict(scratch=P + 64), dict(nbytes=16)])
 def test_router_balance_refuses(bad):
     assert bal(**bad) == ARG
