@@ -24,15 +24,6 @@ __device__ __forceinline__ float warp_max(float v) {
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
-__device__ __forceinline__ void unpack8(const uint4& q, float (&f)[8]) {
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 t = __bfloat1622float2(h[k]);
-    f[2 * k] = t.x;
-    f[2 * k + 1] = t.y;
-  }
-}
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   uint4 q;
   __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&q);
@@ -661,8 +652,6 @@ __global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __res
 // dense part stands, so that no element is rounded twice and an id that appears
 // in several slots gets the sum of their q, in slot order.
 constexpr int KD_MAX_K = 1024;
-constexpr int KD_U = 4;  // 16-byte vectors of a thread per chunk of the ring
-
 struct KdArgs {
   int64_t rows;
   int kcap;  // slots there is room for: K up to a power of two, at least 32
@@ -685,18 +674,18 @@ __device__ __forceinline__ void named_arrive(int n) {
   asm volatile("bar.arrive %0, %1;" ::"n"(ID), "r"(n) : "memory");
 }
 
-template <int CW, int NS>
+template <int CW, int U, int NS>
 constexpr size_t kd_smem(int kcap) {
-  return (size_t)NS * CW * 32 * KD_U * 16 + (size_t)kcap * (2 * 4 + 2) * 4;
+  return (size_t)NS * CW * 32 * U * 16 + (size_t)kcap * (2 * 4 + 2) * 4;
 }
-// CW working warps, a ring of NS chunks, BPS blocks per SM that the registers
-// are to allow.  TWO: both temperatures are summed (hard targets and tau != 1);
+// CW working warps, a ring of NS chunks of U 16-byte vectors a thread, BPS blocks
+// per SM that the registers are to allow.  TWO: both temperatures are summed (hard targets and tau != 1);
 // else one exponential serves both.  Exponentials are taken as 2^(z a - c) with
 // a = log2(e) or log2(e) / tau and the reference c = fl(m a) kept as it is
 // rounded, so that the fused product loses nothing.
-template <int CW, int NS, int BPS, bool TWO>
+template <int CW, int U, int NS, int BPS, bool TWO>
 __global__ void __launch_bounds__((CW + 2) * 32, BPS) distill_k(const KdArgs a) {
-  constexpr int CT = CW * 32, CV = CT * KD_U;  // threads that work on the row; vectors of a chunk
+  constexpr int CT = CW * 32, CV = CT * U;  // threads that work on the row; vectors of a chunk
   extern __shared__ __align__(128) uint8_t smem[];
   uint4* ring = reinterpret_cast<uint4*>(smem);                    // [NS][CV]
   float* slots = reinterpret_cast<float*>(smem + NS * CV * 16);    // two rows' slots, used in turn
@@ -930,18 +919,23 @@ __global__ void __launch_bounds__((CW + 2) * 32, BPS) distill_k(const KdArgs a) 
     for (int c = 0; c < nc; ++c) {
       mbar_wait(&full[slot], ph, failed);
       const uint4* b = ring + slot * CV;
-      uint4 r[KD_U];
+      uint4 r[U];
+      if (c * CV + CV <= nvec) {
 #pragma unroll
-      for (int j = 0; j < KD_U; ++j) {
-        r[j] = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);  // -inf: no probability
-        if (c * CV + j * CT + tid < nvec) r[j] = b[j * CT + tid];
+        for (int j = 0; j < U; ++j) r[j] = b[j * CT + tid];
+      } else {
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          r[j] = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);  // -inf: no probability
+          if (c * CV + j * CT + tid < nvec) r[j] = b[j * CT + tid];
+        }
       }
       if (!held) free_slot();
       step();
       // packed maxima: exact, and NaN passes by (it shows in the sums)
       __nv_bfloat162 mx = __halves2bfloat162(__ushort_as_bfloat16(0xFF80), __ushort_as_bfloat16(0xFF80));
 #pragma unroll
-      for (int j = 0; j < KD_U; ++j) {
+      for (int j = 0; j < U; ++j) {
         const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r[j]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) mx = __hmax2(mx, h[k]);
@@ -964,7 +958,7 @@ __global__ void __launch_bounds__((CW + 2) * 32, BPS) distill_k(const KdArgs a) 
       const float nct = -__fmul_rn(ref, itl), nc1 = -__fmul_rn(ref, kLog2e);
       const f32x2 ct2 = pair2(nct, nct), c12 = pair2(nc1, nc1);
 #pragma unroll
-      for (int j = 0; j < KD_U; ++j) {
+      for (int j = 0; j < U; ++j) {
         const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
 #pragma unroll
         for (int k = 0; k < 4; k += 2) {
@@ -1006,7 +1000,8 @@ __global__ void __launch_bounds__((CW + 2) * 32, BPS) distill_k(const KdArgs a) 
     s1 = warp_sum(s1);
     st = warp_sum(st);
     const bool hard = s_tgt[par] >= 0, soft = s_soft[par];
-    const float f1 = hard ? a.w_ce / s1 : 0.f, ft = soft ? a.w_kd * it / st : 0.f, fs = TWO ? ft : f1 + ft;
+    const float f1 = hard ? __fdividef(a.w_ce, s1) : 0.f, ft = soft ? __fdividef(a.w_kd * it, st) : 0.f;
+    const float fs = TWO ? ft : f1 + ft;
     uint4* dv = reinterpret_cast<uint4*>(a.dlogits + row * V + head);
     const f32x2 ct2 = pair2(-ct, -ct), ft2 = pair2(fs, fs), c12 = pair2(-c1, -c1), f12 = pair2(f1, f1);
     if (held) {
@@ -1016,15 +1011,14 @@ __global__ void __launch_bounds__((CW + 2) * 32, BPS) distill_k(const KdArgs a) 
     for (int c = 0; c < nc; ++c) {
       if (!held) mbar_wait(&full[slot], ph, failed);
       const uint4* b = ring + slot * CV;
-      uint4 r[KD_U];
+      uint4 r[U];  // beyond the row: whatever the ring holds, not stored
 #pragma unroll
-      for (int j = 0; j < KD_U; ++j)
-        if (c * CV + j * CT + tid < nvec) r[j] = b[j * CT + tid];
+      for (int j = 0; j < U; ++j) r[j] = b[j * CT + tid];
       free_slot();
       step();
       if (hard || soft) {
 #pragma unroll
-        for (int j = 0; j < KD_U; ++j) {
+        for (int j = 0; j < U; ++j) {
           const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
           uint32_t o[4];
 #pragma unroll
@@ -1040,11 +1034,17 @@ __global__ void __launch_bounds__((CW + 2) * 32, BPS) distill_k(const KdArgs a) 
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < KD_U; ++j) r[j] = make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < U; ++j) r[j] = make_uint4(0, 0, 0, 0);
       }
+      uint4* out = dv + c * CV + tid;
+      if (c * CV + CV <= nvec) {
 #pragma unroll
-      for (int j = 0; j < KD_U; ++j)
-        if (c * CV + j * CT + tid < nvec) dv[c * CV + j * CT + tid] = r[j];
+        for (int j = 0; j < U; ++j) out[j * CT] = r[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+          if (c * CV + j * CT + tid < nvec) out[j * CT] = r[j];
+      }
     }
     named_arrive<2>(CT + 32);
   }
@@ -1631,7 +1631,7 @@ cudaError_t share_memory_config() {
 
 // Blocks of a distillation kernel that are resident at once, looked up once per
 // device, form and slot room.
-template <int CW, int NS, int BPS, bool TWO>
+template <int CW, int U, int NS, int BPS, bool TWO>
 cudaError_t distill_resident(int kcap, int* out) {
   constexpr int DEV = 16;
   static std::atomic<int> known[DEV][6];
@@ -1642,12 +1642,12 @@ cudaError_t distill_resident(int kcap, int* out) {
   std::atomic<int>* slot = dev < DEV ? &known[dev][ki] : nullptr;
   if (slot && (*out = slot->load(std::memory_order_acquire)) > 0) return cudaSuccess;
   // room for the most slots, so that the setting never shrinks under another call
-  e = cudaFuncSetAttribute(distill_k<CW, NS, BPS, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)kd_smem<CW, NS>(KD_MAX_K));
+  e = cudaFuncSetAttribute(distill_k<CW, U, NS, BPS, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)kd_smem<CW, U, NS>(KD_MAX_K));
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess)
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, distill_k<CW, NS, BPS, TWO>, (CW + 2) * 32,
-                                                      kd_smem<CW, NS>(kcap));
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, distill_k<CW, U, NS, BPS, TWO>, (CW + 2) * 32,
+                                                      kd_smem<CW, U, NS>(kcap));
   if (e != cudaSuccess) return e;
   if (n < 1) return cudaErrorInvalidConfiguration;
   *out = n * sms;
@@ -1655,17 +1655,17 @@ cudaError_t distill_resident(int kcap, int* out) {
   return cudaSuccess;
 }
 
-template <int CW, int NS, int BPS, bool TWO>
+template <int CW, int U, int NS, int BPS, bool TWO>
 cudaError_t launch_distill2(const KdArgs& a, cudaStream_t s) {
   int n = 0;
-  const cudaError_t e = distill_resident<CW, NS, BPS, TWO>(a.kcap, &n);
+  const cudaError_t e = distill_resident<CW, U, NS, BPS, TWO>(a.kcap, &n);
   if (e != cudaSuccess) return e;
   if (n > a.rows) n = (int)a.rows;
-  return launch(distill_k<CW, NS, BPS, TWO>, dim3((unsigned)n), (CW + 2) * 32, kd_smem<CW, NS>(a.kcap), 0, false, s, a);
+  return launch(distill_k<CW, U, NS, BPS, TWO>, dim3((unsigned)n), (CW + 2) * 32, kd_smem<CW, U, NS>(a.kcap), 0, false, s, a);
 }
-template <int CW, int NS, int BPS>
+template <int CW, int U, int NS, int BPS>
 cudaError_t launch_distill(const KdArgs& a, cudaStream_t s) {
-  return a.target && a.tau != 1.f ? launch_distill2<CW, NS, BPS, true>(a, s) : launch_distill2<CW, NS, BPS, false>(a, s);
+  return a.target && a.tau != 1.f ? launch_distill2<CW, U, NS, BPS, true>(a, s) : launch_distill2<CW, U, NS, BPS, false>(a, s);
 }
 
 cudaError_t launch_few_bwd(const bf16* h, const bf16* W, const int32_t* target, int T, int H, int V, float g,
@@ -1787,26 +1787,30 @@ cudaError_t distill_topk(const bf16* logits, const int32_t* target, const float*
   const KdArgs a{rows, kcap, logits, target, t_val, t_idx, V, K, tau, w_ce, w_kd, row_ce, row_kd, dlogits};
   // working warps of a block, by the row's length and the number of rows; each
   // rule with both sides measured (us, GB300)
-  //   many rows: one warp and 12 blocks per SM up to 12288 columns (8192 rows of
-  //   12288: 88 against 95 with four warps; of 16384: 125 against 102), four up
-  //   to 24576 (of 24576: 157 against 183 with eight; of 28000: 177 against 170),
-  //   eight up to 65536 (4096 rows of 64000: 196 against 209 with sixteen; of
-  //   80000: 252 against 214, where two rows per SM no longer stay in L2 until
-  //   they are read again)
-  int warps = V <= 12288 ? 1 : V <= 24576 ? 4 : V <= 65536 ? 8 : 16;
+  //   many rows: one warp and 12 blocks per SM up to 7168 columns (16384 rows of
+  //   7000: 114 against 118 with two warps; 8192 rows of 10000: 81 against 67),
+  //   two up to 15360 (8192 rows of 14336: 95 against 98 with four; of 16384: 110
+  //   against 101), four up to 24576, with two temperatures, where the
+  //   exponentials weigh more, up to 40960 (8192 rows of 28000: 177 against 170
+  //   with eight; 4096 of 36000 with two temperatures: 113 against 129, of 45000:
+  //   161 against 149), eight up to 65536 (4096 rows of 64000: 194 against 208
+  //   with sixteen; of 80000: 252 against 214, where two rows per SM no longer
+  //   stay in L2 until they are read again)
+  const bool two = target && tau != 1.f;
+  int warps = V <= 7168 ? 1 : V <= 15360 ? 2 : V <= (two ? 40960 : 24576) ? 4 : V <= 65536 ? 8 : 16;
   //   few rows, so that a row's own time counts: four warps while their 608
   //   blocks take all rows at once (304 rows of 4096: 4.6 against 6.7 with one;
-  //   600: 7.8 against 9.2; 1200: 11.4 against 10.4), with long rows for four
-  //   times as many (2400 rows of 8192: 22.6 against 28.2); eight while 304 do
-  //   (152 rows of 24000: 6.0 against 7.0 with four), sixteen while 152 do (152
-  //   rows of 48000: 8.2 against 8.8 with eight)
-  if (V > 2048 && warps < 4 && (rows <= 608 || (V >= 8192 && rows <= 2432))) warps = 4;
+  //   600: 7.8 against 9.2; 1200: 11.4 against 10.4), eight while 304 do (152 rows
+  //   of 24000: 6.0 against 7.0 with four), sixteen while 152 do (152 rows of
+  //   48000: 8.2 against 8.8 with eight)
+  if (V > 2048 && warps < 4 && rows <= 608) warps = 4;
   if (V > 16384 && warps < 8 && rows <= 304) warps = 8;
   if (V > 32768 && rows <= 152) warps = 16;
-  if (warps == 1) return launch_distill<1, 6, 12>(a, s);
-  if (warps == 4) return launch_distill<4, 6, 4>(a, s);
-  if (warps == 8) return launch_distill<8, 6, 2>(a, s);
-  return launch_distill<16, 5, 1>(a, s);
+  if (warps == 1) return launch_distill<1, 4, 6, 12>(a, s);
+  if (warps == 2) return launch_distill<2, 4, 6, 8>(a, s);
+  if (warps == 4) return launch_distill<4, 4, 6, 4>(a, s);
+  if (warps == 8) return launch_distill<8, 4, 6, 2>(a, s);
+  return launch_distill<16, 4, 5, 1>(a, s);
 }
 
 size_t router_balance_scratch(int64_t T, int S, int E) {
