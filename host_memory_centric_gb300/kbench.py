@@ -7,6 +7,9 @@ python -m host_memory_centric_gb300.kbench attn_fwd --S 2048 --nseq 4 --nh 16 --
 python -m host_memory_centric_gb300.kbench attn_bwd --S 2048 --nseq 4 --nh 16 --nkv 4 --hd 128
 python -m host_memory_centric_gb300.kbench rmsnorm_bwd --T 8192 --H 2048
 python -m host_memory_centric_gb300.kbench cross_entropy --T 8192 --V 32000
+python -m host_memory_centric_gb300.kbench linear_cross_entropy --T 8192 --H 2048 --V 32000
+python -m host_memory_centric_gb300.kbench distill_topk --T 8192 --V 32000 --topk 32 --tau 2
+python -m host_memory_centric_gb300.kbench router_balance --T 16384 --E 32 --k 4
 python -m host_memory_centric_gb300.kbench moe_ffn --T 16384 --H 2880 --E 32 --k 4 --Fe 2880
 python -m host_memory_centric_gb300.kbench layer_gemms --config 7.6b
 """
@@ -53,6 +56,8 @@ def main():
     ap.add_argument("--E", type=int, default=32)
     ap.add_argument("--k", type=int, default=4)
     ap.add_argument("--Fe", type=int, default=2880)
+    ap.add_argument("--topk", type=int, default=32, help="distill_topk: teacher's logits per row")
+    ap.add_argument("--tau", type=float, default=2.0, help="distill_topk: temperature")
     ap.add_argument("--config", default="7.6b")
     ap.add_argument("--no-head", action="store_true", help="layer_gemms: leave out the LM-head forms")
     ap.add_argument("--gemm-mode", type=int, default=-1,
@@ -136,6 +141,37 @@ def main():
         ms = timeit(lambda: ops.cross_entropy(z, tgt, 1.0 / a.T, rl), a.iters, a.warmup)
         by = 4.0 * a.T * V
         res.update(shape=[a.T, V], ms=ms, gbs=by / ms / 1e6)
+    elif a.op == "linear_cross_entropy":
+        # the LM head, its loss and both gradients in one call, every token with a target
+        T, H, V = a.T, a.H, a.V
+        h = torch.randn(T, H, device=dev).to(bf)
+        W = (torch.randn(V, H, device=dev) * (2.5 / H ** 0.5)).to(bf)
+        tgt = torch.randint(0, V, (T,), dtype=torch.int32, device=dev)
+        rl, dh, dW = torch.empty(T, device=dev), torch.empty_like(h), torch.empty_like(W)
+        sc = torch.empty(ops.linear_cross_entropy_scratch_bytes(T, H, V), dtype=torch.uint8, device=dev)
+        ms = timeit(lambda: ops.linear_cross_entropy(h, W, tgt, 1.0 / T, rl, dh, dW, sc), a.iters, a.warmup)
+        res.update(shape=[T, H, V], ms=ms, tflops=6.0 * T * H * V / ms / 1e9, gbs=4.0 * (T + V) * H / ms / 1e6)
+    elif a.op == "distill_topk":
+        # --T rows of --V logits, targets and the teacher's --topk largest logits at --tau
+        T, V, K = a.T, a.V, a.topk
+        z = (torch.randn(T, V, device=dev) * 2.5).to(bf)
+        val, ids = torch.topk(z.float() + torch.randn(T, V, device=dev), K, dim=1)
+        ids = ids.to(torch.int32).contiguous()
+        tgt = torch.randint(0, V, (T,), dtype=torch.int32, device=dev)
+        ce, kd, dz = torch.empty(T, device=dev), torch.empty(T, device=dev), torch.empty_like(z)
+        ms = timeit(lambda: ops.distill_topk(z, tgt, val, ids, a.tau, 0.5 / T, 0.5 * a.tau ** 2 / T, ce, kd, dz),
+                    a.iters, a.warmup)
+        res.update(shape=[T, V, K], tau=a.tau, ms=ms, gbs=4.0 * T * V / ms / 1e6)
+    elif a.op == "router_balance":
+        # balance and z loss of --T tokens, --E experts, --k choices each, one group
+        T, E, k = a.T, a.E, a.k
+        z = torch.randn(T, E, device=dev) * 1.5
+        idx = torch.topk(z, k, dim=1).indices.to(torch.int32).contiguous()
+        loss, cnt = torch.empty(2, device=dev), torch.empty(1, E, dtype=torch.int32, device=dev)
+        pr, dz = torch.empty(1, E, device=dev), torch.empty(T, E, dtype=bf, device=dev)
+        sc = torch.empty(ops.router_balance_scratch_bytes(T, T, E), dtype=torch.uint8, device=dev)
+        ms = timeit(lambda: ops.router_balance(z, idx, None, T, 0.01, 0.001, loss, cnt, pr, dz, sc), a.iters, a.warmup)
+        res.update(shape=[T, E, k], ms=ms, gbs=(6.0 * T * E + 4.0 * T * k) / ms / 1e6)
     elif a.op == "moe_ffn":
         # one MoE feed-forward, forward and backward (router, routing, grouped expert GEMMs, combine);
         # includes one host synchronisation for the per-expert counts
