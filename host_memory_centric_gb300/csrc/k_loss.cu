@@ -150,6 +150,15 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t n
                "l"(src), "r"(n), "r"(su32(bar))
                : "memory");
 }
+// Between this thread's loads from a stage of a ring of such copies and the
+// barrier that frees it.  The barrier orders plain accesses only; without the
+// fence the next copy came before loads that stood in a queue behind stores
+// (8192 rows of 32000 columns: 20 to 60 thousand elements of the gradient were
+// those of a later chunk).  Distillation is as
+// fast with it; the balance loss takes 2 us more for 131072 tokens of 128 experts.
+__device__ __forceinline__ void reads_before_copies() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
 __device__ __forceinline__ void async_load4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(su32(dst)), "l"(src) : "memory");
 }
@@ -563,6 +572,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __res
     // may be no number
     for (int i = n * (WROW / 16) + tid; i < SUB * (WROW / 16); i += FEW_THREADS)
       reinterpret_cast<uint4*>(smem + (k % FEW_STAGES) * STAGE)[i] = make_uint4(0, 0, 0, 0);
+    reads_before_copies();
     __syncthreads();  // also: every warp is done with the stage before, which takes a new one
     if (warp == 0 && k >= 1 && k - 1 + FEW_STAGES < stages) fill(k - 1 + FEW_STAGES);
     if (ncol <= 0 || rg * 16 >= n) continue;
@@ -905,6 +915,7 @@ __global__ void __launch_bounds__((CW + 2) * 32, BPS) distill_k(const KdArgs a) 
     }
   };
   auto free_slot = [&] {
+    reads_before_copies();
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[slot]);
   };
@@ -1253,6 +1264,7 @@ __global__ void __launch_bounds__(BAL_THREADS, NV == 1 ? 2 : 1) balance_grad_k(c
     if (VEC) mbar_wait(&full[turn % BAL_STAGES], (uint32_t)(turn / BAL_STAGES) & 1, failed);
     load(turn, now);
     if (VEC) {
+      reads_before_copies();
       __syncthreads();  // every lane has its part: the stage takes the next chunk
       if (tid == 0 && turn + BAL_STAGES < chunks) fill(turn + BAL_STAGES);
     }

@@ -212,6 +212,15 @@ def test_linear_cross_entropy_same_bits_twice_and_on_another_stream(T):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("T", [4, 16])
+def test_linear_cross_entropy_few_tokens_refilled_ring_under_load(T):
+    h, W, tgt = lce_inputs(T, 2048, 100000, 15)
+    want = run_lce(h, W, tgt, 0.5)
+    for _ in range(20):
+        for x, y in zip(run_lce(h, W, tgt, 0.5), want):
+            assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("T", [8, 520])
 def test_linear_cross_entropy_two_graphs_replayed_at_once(T):
     """Two captured calls with a workspace each, replayed on two streams at the same time with new inputs."""
@@ -394,6 +403,21 @@ def test_distill_same_bits_twice_and_captured():
     assert torch.equal(ce, want[0]) and torch.equal(kd, want[1]) and torch.equal(d, want[2])
 
 
+# rows longer than each form's ring (1, 2, 4, 8 and 16 working warps), enough of them that every block takes several
+# and the stores of the gradient are the limit: chunks are refilled while loads and stores wait in line
+@pytest.mark.parametrize("R,V,tau,hard", [(16384, 7000, 1.0, True), (12288, 14000, 1.5, False), (8192, 32000, 2.0, True),
+                                          (4096, 60000, 1.0, False), (2048, 152064, 1.3, True)])
+def test_distill_refilled_rings_under_load(R, V, tau, hard):
+    z, tgt, y, ids = kd_inputs(R, V, 32, 95, hard)
+    got = run_kd(z, tgt, y, ids, tau, 0.4, 0.6)
+    some = torch.arange(5, R, R // 256, device="cuda")
+    check_kd(z[some], tgt[some] if hard else None, y[some], ids[some], tau, 0.4, 0.6,
+             tuple(None if t is None else t[some] for t in got))
+    for _ in range(10):
+        for a, b in zip(run_kd(z, tgt, y, ids, tau, 0.4, 0.6), got):
+            assert (a is None and b is None) or torch.equal(a, b)
+
+
 def test_distill_gradient_matches_differences():
     z, tgt, y, ids = kd_inputs(6, 300, 7, 90)
     _, _, d = run_kd(z, tgt, y, ids, 1.5, 0.5, 1.0)
@@ -517,6 +541,14 @@ def test_router_balance_same_bits_twice_and_captured(T, S, E, k):
     torch.cuda.synchronize()
     for x, y, o in zip(want, again, outs):
         assert torch.equal(x, y) and torch.equal(x, o)
+
+
+def test_router_balance_refilled_ring_under_load():
+    z, idx = bal_inputs(131072, 128, 8, 135)
+    want = run_bal(z, idx, None, 32768, 0.01, 0.001)
+    for _ in range(20):
+        for x, y in zip(run_bal(z, idx, None, 32768, 0.01, 0.001), want):
+            assert torch.equal(x, y)
 
 
 def test_router_balance_gradient_matches_differences():
