@@ -82,11 +82,10 @@ struct Epi {
   int tiles_m, tiles_n, group_m;
   int a_mn, b_mn;
   // gradient epilogue (EPI 3) only: D = bf16(alpha acc); with ksplit > 1 the K
-  // blocks are cut into ksplit runs of kb_per, run i's product going to
-  // Dacc + i * slab (FP32) instead
+  // blocks are cut into ksplit runs of kb_per, run i's product going to slab i
+  // of Dacc (FP32) instead
   float alpha;
   int ksplit, kb_per;
-  int64_t slab;
 };
 
 constexpr int MAX_EXPERT_GROUPS = 128;
@@ -115,7 +114,7 @@ struct Params {
   int grp_e[MAX_EXPERT_GROUPS], grp_k0[MAX_EXPERT_GROUPS], grp_nk[MAX_EXPERT_GROUPS];
   SoftmaxPieces sp;   // softmax epilogue (gemm_softmax_pieces)
   CUtensorMap td[2];  // D of each group, for the gradient epilogue's stores
-  int store[2];       // whether the group's D goes through td (a plain BF16 result)
+  int store[2];       // whether the group's result goes through td: 1 BF16 D, 2 FP32 slabs
 };
 
 __device__ __forceinline__ uint32_t su32(const void* p) {
@@ -390,6 +389,38 @@ __device__ __forceinline__ void store_tile(const CUtensorMap* map, float alpha, 
   }
 }
 
+__device__ __forceinline__ void tma_store3(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"((uint64_t)map),
+               "r"(x), "r"(y), "r"(z), "r"(su32(src))
+               : "memory");
+}
+// The same for one run of a split sum: FP32, 32 columns at a time, to slab
+// `run` of [runs][M][N].
+__device__ __forceinline__ void store_tile_f32(const CUtensorMap* map, int row0, int col0, int run, int M, int N,
+                                               uint32_t taddr, uint8_t* buf, int lane, int& turn) {
+  if (row0 >= M || col0 >= N) return;  // warp-uniform
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    if (col0 + c * 32 >= N) break;
+    uint32_t r[32];
+    tmem_ld32(taddr + (uint32_t)(c * 32), r);
+    uint8_t* b = buf + (turn & 1) * 4096;
+    if (lane == 0) store_wait_read<1>();
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<uint4*>(b + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+          make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+      tma_store3(map, b, col0 + c * 32, row0, run);
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+    ++turn;
+  }
+}
+
 // Softmax epilogue of one row of a piece of 128 columns of logits (columns col0
 // .. of N, in TMEM from taddr on): m = the row's largest logit of the piece, s =
 // sum exp(z - m) over its columns but the target's (which the join adds from
@@ -398,15 +429,15 @@ __device__ __forceinline__ void store_tile(const CUtensorMap* map, float alpha, 
 // the piece, to zt; if wanted, fp16(2^15 exp(z - m)) to E (11 bits down to 20
 // nats below the piece's maximum; BF16 would round every gradient element a
 // second time as coarsely as the first).  The piece is held in registers
-// between the maximum and the exponentials.  Bound by the four SM quarters'
-// issue slots (about 6 a value), hidden behind the next tile's MMAs from H of
-// about 700 on.  All lanes take part in the loads; rows >= M store nothing.
+// between the maximum and the exponentials (read from TMEM twice in loops of 32
+// columns, each load waited for, a tile took half as long again: 35 against 22
+// us for 3138 tokens of 96 by 5585).  Hidden behind the next tile's MMAs from H
+// of about 700 on.  All lanes take part in the loads; rows >= M store nothing.
 template <bool STORE>
-__device__ __forceinline__ void softmax_piece(const SoftmaxPieces& sp, const CUtensorMap* map, int row, int lane, int M,
-                                              int N, int col0, uint32_t taddr, uint8_t* buf, int& turn) {
+__device__ __forceinline__ void softmax_piece(const SoftmaxPieces& sp, const CUtensorMap* map, int row, int tgt, int lane,
+                                              int M, int N, int col0, uint32_t taddr, uint8_t* buf, int& turn) {
   if (row - lane >= M || col0 >= N) return;  // warp-uniform
   const bool live = row < M;
-  const int tgt = live ? sp.target[row] : -1;
   uint32_t r[4][32];
 #pragma unroll
   for (int c = 0; c < 4; ++c) tmem_ld32_nw(taddr + (uint32_t)(c * 32), r[c]);
@@ -420,43 +451,47 @@ __device__ __forceinline__ void softmax_piece(const SoftmaxPieces& sp, const CUt
       for (int i = 0; i < 32; ++i)
         if (c * 32 + i >= left) r[c][i] = 0xff800000u;  // -inf
   }
-  const int ti = tgt - col0;  // the target's place in the piece
-  const bool mine = ti >= 0 && ti < 128 && tgt < N;
-  float m0 = -INFINITY, m1 = -INFINITY;
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
+  for (int i = 0; i < 32; ++i)
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      m0 = fmaxf(m0, __uint_as_float(r[c][i]));
-      m1 = fmaxf(m1, __uint_as_float(r[c][i + 1]));
-    }
-  const float m = fmaxf(m0, m1);
+    for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(r[c][i]));
+  const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
   // every logit -inf (or NaN): the reference 0 leaves exp(z) = 0 (or NaN)
   const float ref = m == -INFINITY ? 0.f : m;
-  if (__any_sync(0xffffffffu, mine)) {  // once per row and pass over V
+  const int ti = live && tgt < N ? tgt - col0 : -1;  // the target's place in the piece
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+  for (int c = 0; c < 4; ++c) {
+    if (!__any_sync(0xffffffffu, ti >> 5 == c)) continue;  // some row's target: once per row and pass over V
+    float z = 0.f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (mine && ti == c * 32 + i) {
-          sp.zt[row] = __uint_as_float(r[c][i]);
-          r[c][i] = 0xff800000u;  // out of the sum; the join writes its gradient
-        }
+    for (int i = 0; i < 32; ++i)
+      if (ti == c * 32 + i) {
+        z = __uint_as_float(r[c][i]);
+        r[c][i] = 0xff800000u;  // out of the sum; the join writes its gradient
+      }
+    if (ti >> 5 == c) sp.zt[row] = z;
   }
-  float s0 = 0.f, s1 = 0.f;
+  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
   // z - m first, exact for the terms that count, then the factor log2(e): a
   // fused z log2(e) - m log2(e) would lose digits where |z| is large
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const float a = exp2_approx(fmaf(__uint_as_float(r[c][i]) - ref, kLog2e, 15.f));
-      const float b = exp2_approx(fmaf(__uint_as_float(r[c][i + 1]) - ref, kLog2e, 15.f));
-      s0 += a;
-      s1 += b;
-      if (STORE) r[c][i >> 1] = pack_half(a, b);
+    for (int i = 0; i < 32; i += 4) {
+      float x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = exp2_approx(fmaf(__uint_as_float(r[c][i + k]) - ref, kLog2e, 15.f));
+      s0 += x[0];
+      s1 += x[1];
+      s2 += x[2];
+      s3 += x[3];
+      if (STORE) {
+        r[c][i >> 1] = pack_half(x[0], x[1]);
+        r[c][(i >> 1) + 1] = pack_half(x[2], x[3]);
+      }
     }
-  if (live) sp.stat[(int64_t)row * sp.npieces + col0 / 128] = make_float2(ref, (s0 + s1) * 0x1p-15f);
+  if (live) sp.stat[(int64_t)row * sp.npieces + col0 / 128] = make_float2(ref, ((s0 + s1) + (s2 + s3)) * 0x1p-15f);
   if (STORE) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -958,6 +993,9 @@ __global__ void __launch_bounds__(p_threads<EPI>(), 1) gemm_pair_kernel(const __
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr int ST = p_ring<NW, EPI>();
+  // tiles that every role knows without the ring: with EPI, a pair's first (the
+  // launch has no more pairs than tiles); announcing it took 0.8 us of a short launch
+  constexpr int FIRST = EPI == 0 ? 0 : 1;
   constexpr int EW = EPI == 0 ? 4 : 8;            // epilogue warps
   constexpr int EC = BN * NW / (EPI == 0 ? 1 : 2);  // columns of a tile each of them takes
   constexpr int RING = EPI >= 2 ? 5 * P_STAGE_BYTES : P_STAGES * P_STAGE_BYTES;
@@ -1030,10 +1068,13 @@ __global__ void __launch_bounds__(p_threads<EPI>(), 1) gemm_pair_kernel(const __
       const int tickets = (num_tiles > ncl ? num_tiles - ncl : 0) + ncl;
       int ahead = -1;  // the ticket drawn one tile ahead (its latency hides behind the current tile's loads)
       for (int i = 0; ok && !p.stall; ++i) {
-        const int slot = i % P_TRING;
-        const uint32_t ph = (uint32_t)(i / P_TRING) & 1;
+        const int slot = (i - FIRST) % P_TRING;
+        const uint32_t ph = (uint32_t)((i - FIRST) / P_TRING) & 1;
         int tile;
-        if (leader) {
+        if (i < FIRST) {
+          tile = cl;
+          if (leader && p.tile_ctr) ahead = atomicAdd(p.tile_ctr, 1);
+        } else if (leader) {
           if (!mbar_wait(&tid_empty[slot], ph ^ 1, abort_flag)) {
             ok = false;
             break;
@@ -1091,13 +1132,16 @@ __global__ void __launch_bounds__(p_threads<EPI>(), 1) gemm_pair_kernel(const __
       uint32_t phase = 0;
       bool ok = true;
       for (int it = 0;; ++it) {
-        const int slot = it % P_TRING;
-        if (!mbar_wait(&tid_full[slot], (uint32_t)(it / P_TRING) & 1, abort_flag)) {
-          ok = false;
-          break;
+        int tile = cl;
+        if (it >= FIRST) {
+          const int slot = (it - FIRST) % P_TRING;
+          if (!mbar_wait(&tid_full[slot], (uint32_t)((it - FIRST) / P_TRING) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tile = tid_ring[slot];
+          mbar_arrive(&tid_empty[slot]);
         }
-        int tile = tid_ring[slot];
-        mbar_arrive(&tid_empty[slot]);
         if (tile < 0) break;
         // two 256-column accumulators, or one of 512 columns for wide tiles
         const int acc = NW == 1 ? (it & 1) : 0;
@@ -1132,49 +1176,53 @@ __global__ void __launch_bounds__(p_threads<EPI>(), 1) gemm_pair_kernel(const __
     if (EPI != 0) dep_wait();  // nothing of the kernels before may still be read, or not yet written
     bool ok = true;
     for (int it = 0;; ++it) {
-      const int slot = it % P_TRING;
-      // warp-uniform outcomes: the TMEM loads below are warp-collective
-      if (!__all_sync(0xffffffffu, mbar_wait_cl(&tid_full[slot], (uint32_t)(it / P_TRING) & 1, abort_flag))) {
-        ok = false;
-        break;
+      int tile = cl;
+      if (it >= FIRST) {
+        const int slot = (it - FIRST) % P_TRING;
+        // warp-uniform outcomes: the TMEM loads below are warp-collective
+        if (!__all_sync(0xffffffffu, mbar_wait_cl(&tid_full[slot], (uint32_t)((it - FIRST) / P_TRING) & 1, abort_flag))) {
+          ok = false;
+          break;
+        }
+        tile = tid_ring[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(cluster_addr(&tid_empty[slot], 0));
       }
-      const int tile = tid_ring[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(cluster_addr(&tid_empty[slot], 0));
       if (tile < 0) break;
       const int acc = NW == 1 ? (it & 1) : 0;
       const uint32_t aph = NW == 1 ? (uint32_t)((it >> 1) & 1) : (uint32_t)(it & 1);
+      const Epi& e = (NG == 1 || tile < split) ? p.e[0] : p.e[1];
+      int tm, tn, local = (NG == 1 || tile < split) ? tile : tile - split, run, kb0, nk;
+      tile_run<EPI>(e, local, run, kb0, nk);
+      pair_tile_mn(local, e, tm, tn);
+      const int row = tm * 2 * BM + (int)rank * BM + row_in_tile;
+      int tgt = -1;  // the row's target, on its way during the wait
+      if constexpr (EPI == 1 || EPI == 2) {
+        if (row < e.M) tgt = p.sp.target[row];
+      }
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], aph, abort_flag))) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const Epi& e = (NG == 1 || tile < split) ? p.e[0] : p.e[1];
-      int tm, tn, local = (NG == 1 || tile < split) ? tile : tile - split, run, kb0, nk;
-      tile_run<EPI>(e, local, run, kb0, nk);
-      pair_tile_mn(local, e, tm, tn);
-      Epi er;
-      if constexpr (EPI == 3) {
-        er = e;
-        if (e.ksplit > 1) er.Dacc += run * e.slab;
-      }
-      const int row = tm * 2 * BM + (int)rank * BM + row_in_tile;
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
       const int col0 = tn * BN * NW + half * EC;
       const uint32_t tcol = taddr + (uint32_t)(half * EC);
       if constexpr (EPI == 1 || EPI == 2) {
-        softmax_piece<EPI == 2>(p.sp, &p.td[0], row, lane, e.M, e.N, col0, tcol, store_buf, store_turn);
+        softmax_piece<EPI == 2>(p.sp, &p.td[0], row, tgt, lane, e.M, e.N, col0, tcol, store_buf, store_turn);
       } else {
         const int grp = (NG == 1 || tile < split) ? 0 : 1;
-        if (EPI == 3 && p.store[grp]) {
+        if (EPI == 3 && p.store[grp] == 1) {
           store_tile(&p.td[grp], e.alpha, row - lane, col0, e.M, e.N, tcol, store_buf, lane, store_turn);
+        } else if (EPI == 3 && p.store[grp] == 2) {
+          store_tile_f32(&p.td[grp], row - lane, col0, run, e.M, e.N, tcol, store_buf, lane, store_turn);
         } else {
           for (int c = 0; c < EC / 32; ++c) {
             uint32_t r[32];
             tmem_ld32(tcol + (uint32_t)(c * 32), r);
             const int col = col0 + c * 32;
             if (row < e.M && col < e.N) {
-              if constexpr (EPI == 3) epi_store<true>(er, row, col, r);
+              if constexpr (EPI == 3) epi_store<true>(e, row, col, r);
               else epi_store(e, row, col, r);
             }
           }
@@ -1309,6 +1357,18 @@ bool make_map3(CUtensorMap* m, const bf16* base, int64_t rows, int64_t cols, int
   CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16*>(base), dims, strides, box,
                         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// 3-D FP32 tensor map of n matrices [rows][cols] behind one another, box {32, 32, 1}.
+bool make_map_f32(CUtensorMap* m, float* base, int64_t rows, int64_t cols, int64_t n) {
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)n};
+  const cuuint64_t strides[2] = {(cuuint64_t)cols * 4, (cuuint64_t)(rows * cols) * 4};
+  const cuuint32_t box[3] = {32, 32, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -1633,7 +1693,8 @@ cudaError_t gemm_grads(const GradArgs& g, cudaStream_t s) {
       ep.kb_per = (nk + g.ksplit - 1) / g.ksplit;
       ep.ksplit = (nk + ep.kb_per - 1) / ep.kb_per;
       if (ep.ksplit != g.ksplit) return cudaErrorInvalidValue;
-      ep.slab = (int64_t)ep.M * ep.N;
+      if (!make_map_f32(&p.td[i], g.slabs, ep.M, ep.N, ep.ksplit)) return cudaErrorInvalidValue;
+      p.store[i] = 2;
     }
     if (w.D && !w.acc_mode && !w.R) {  // a plain result: box of 64 columns by a warp's 32 rows
       if (!make_map(&p.td[i], w.D, w.M, w.N, w.ldd, 32)) return cudaErrorInvalidValue;

@@ -206,21 +206,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) ce_join_k(const float2* __restri
       for (int v = first; v < nvec; v += step) e[v] = make_uint4(0, 0, 0, 0);
     return;
   }
+  // the first vectors are on their way while the statistics are joined
   const float2* st = stat + row * npieces;
-  float m = -INFINITY;
-  for (int p = threadIdx.x; p < npieces; p += JOIN_THREADS) m = fmaxf(m, st[p].x);
-  const float M = block_max<JOIN_THREADS>(m, red);
-  float s = 0.f;
-  for (int p = threadIdx.x; p < npieces; p += JOIN_THREADS) s += st[p].y * expf(st[p].x - M);
-  const float rest = block_sum<JOIN_THREADS>(s, red);
-  const float z = zt[row], et = expf(z - M), S = rest + et;
-  if (threadIdx.x == 0 && blockIdx.y == 0) row_loss[row] = z == M ? log1pf(rest) : (M - z) + logf(S);
-  if (!E) return;
-  const float scale = 0x1p-15f / S, dt = -rest / S;
   constexpr int U = 4;  // vectors of a thread on their way at a time
-  for (int v = first; v < nvec; v += U * step) {
-    uint4 q[U];
-    float f[U];
+  uint4 q[U];
+  float f[U];
+  auto load = [&](int v) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int w = v + u * step;
@@ -229,16 +220,30 @@ __global__ void __launch_bounds__(JOIN_THREADS) ce_join_k(const float2* __restri
         f[u] = st[w >> 4].x;
       }
     }
+  };
+  const float z = zt[row];
+  if (E) load(first);
+  float m = -INFINITY;
+  for (int p = threadIdx.x; p < npieces; p += JOIN_THREADS) m = fmaxf(m, st[p].x);
+  const float M = block_max<JOIN_THREADS>(m, red);
+  float s = 0.f;
+  for (int p = threadIdx.x; p < npieces; p += JOIN_THREADS) s += st[p].y * expf(st[p].x - M);
+  const float rest = block_sum<JOIN_THREADS>(s, red);
+  const float et = expf(z - M), S = rest + et;
+  if (threadIdx.x == 0 && blockIdx.y == 0) row_loss[row] = z == M ? log1pf(rest) : (M - z) + logf(S);
+  if (!E) return;
+  const float scale = 0x1p-15f / S, dt = -rest / S;
+  for (int v = first; v < nvec; v += U * step) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int w = v + u * step;
       if (w >= nvec) continue;
       const float k = expf(f[u] - M) * scale;
-      const __half2* h = reinterpret_cast<const __half2*>(&q[u]);
+      const __half2* h2 = reinterpret_cast<const __half2*>(&q[u]);
       float x[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 t = __half22float2(h[i]);
+        const float2 t = __half22float2(h2[i]);
         x[2 * i] = t.x * k;
         x[2 * i + 1] = t.y * k;
       }
@@ -249,6 +254,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) ce_join_k(const float2* __restri
       }
       e[w] = pack8(x);
     }
+    load(v + U * step);
   }
 }
 
