@@ -562,6 +562,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __res
     const int b = r0 + k * SUB, n = min(SUB, r1 - b);
     bf16* dT = reinterpret_cast<bf16*>(dbuf + (k & 1) * 2 * few_d_bytes(H));  // [SUB][16]
     bf16* dN = dT + SUB * 16;                                                 // [16][SUB]
+    reads_before_copies();  // those of the stage before, all used by now
     mbar_wait(&full[k % FEW_STAGES], (uint32_t)(k / FEW_STAGES) & 1, failed);
     for (int i = tid; i < FEW_T * SUB; i += FEW_THREADS) {  // the logits' gradient
       const int t = i / SUB, r = i % SUB;
@@ -578,7 +579,6 @@ __global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __res
     // may be no number
     for (int i = n * (WROW / 16) + tid; i < SUB * (WROW / 16); i += FEW_THREADS)
       reinterpret_cast<uint4*>(smem + (k % FEW_STAGES) * STAGE)[i] = make_uint4(0, 0, 0, 0);
-    reads_before_copies();
     __syncthreads();  // also: every warp is done with the stage before, which takes a new one
     if (warp == 0 && k >= 1 && k - 1 + FEW_STAGES < stages) fill(k - 1 + FEW_STAGES);
     if (ncol <= 0 || rg * 16 >= n) continue;
@@ -1269,11 +1269,6 @@ __global__ void __launch_bounds__(BAL_THREADS, NV == 1 ? 2 : 1) balance_grad_k(c
     const bool now = on;
     if (VEC) mbar_wait(&full[turn % BAL_STAGES], (uint32_t)(turn / BAL_STAGES) & 1, failed);
     load(turn, now);
-    if (VEC) {
-      reads_before_copies();
-      __syncthreads();  // every lane has its part: the stage takes the next chunk
-      if (tid == 0 && turn + BAL_STAGES < chunks) fill(turn + BAL_STAGES);
-    }
     src += (int64_t)RPB * E;
     if (val) val += RPB;
     on = r + RPB < r1 && (!val || *val);
@@ -1284,6 +1279,11 @@ __global__ void __launch_bounds__(BAL_THREADS, NV == 1 ? 2 : 1) balance_grad_k(c
       m = fmaxf(m, fmaxf(t.x, t.y));
     }
     m = over_row(m, mx);
+    if (VEC) {
+      reads_before_copies();
+      __syncthreads();  // every lane has its part: the stage takes the next chunk
+      if (tid == 0 && turn + BAL_STAGES < chunks) fill(turn + BAL_STAGES);
+    }
     // 2^(x log2(e) - c) with c = fl(m log2(e)): the rounding of c cancels.  Padded
     // rows and lanes beyond E hold -inf, whose exponential is 0.
     const float c = m == -INFINITY ? 0.f : __fmul_rn(m, kLog2e);
