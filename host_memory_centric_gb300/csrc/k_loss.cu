@@ -433,13 +433,15 @@ __host__ __device__ constexpr int few_sub(int H) { return 16 * few_groups(H); } 
 // bytes from row to row of W in a stage: 16 more than the columns' own, so that
 // the eight rows an ldmatrix reads lie in different banks
 __host__ __device__ constexpr int few_wrow(int H) { return FEW_COLS * 2 / few_groups(H) + 16; }
-// A stage: rows of W in BF16, then the tokens' z of these rows in FP32.
-__host__ __device__ constexpr int few_stage(int T, int H) {
-  return (few_sub(H) * few_wrow(H) + T * few_sub(H) * 4 + 127) / 128 * 128;
+// A stage: rows of W in BF16, where dh is made of them, then the tokens' z of these rows in FP32.
+__host__ __device__ constexpr int few_stage(int T, int H, bool dh) {
+  return ((dh ? few_sub(H) * few_wrow(H) : 0) + T * few_sub(H) * 4 + 127) / 128 * 128;
 }
 // After the ring, for two stages in turn: d in BF16, [rows][16 tokens] and [16 tokens][rows].
 __host__ __device__ constexpr int few_d_bytes(int H) { return few_sub(H) * 16 * 2; }
-__host__ __device__ constexpr int few_smem(int T, int H) { return FEW_STAGES * few_stage(T, H) + 4 * few_d_bytes(H); }
+__host__ __device__ constexpr int few_smem(int T, int H, bool dh) {
+  return FEW_STAGES * few_stage(T, H, dh) + 4 * few_d_bytes(H);
+}
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const void* p) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -454,22 +456,351 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], const void* p) {
                : "memory");
 }
 
+__device__ __forceinline__ void mma_bf16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0));
+}
+
+// One pass over W for z, the statistics and dh:
+//   dh_t = g (sum_{v != target} p_v W_v - (rest / S) W_target)
+// needs p only up to a factor per token, so each block keeps sums of exp(z_v - m)
+// W_v around its running maximum m, moved when m rises, and ce_few_dh adds the
+// blocks' sums with their factors exp(m - M) / S.  W is then read once and dW
+// written once, which is the floor; with a second pass over W 5 tokens of 3584 by
+// 152064 took 558 us.  A stage is eight whole rows: the warps take a slice of the
+// columns each, h of it in registers as the first factor of z, the sums of dh in
+// registers too (their columns as the rows of the mma, tokens as its columns).
+// The warps' parts of z meet in shared memory, every warp adds them for itself in
+// the layout in which exp(z - m) is then its second factor of dh: one barrier a
+// stage.  W comes out of shared memory twice, once transposed.
+// NT: groups of eight tokens; KP: groups of 32 columns that a warp has.
+// RB: groups of eight rows in a stage.  Of the last OUT column groups h stays in
+// shared memory, in the order of the fragments, where the registers do not reach.
+constexpr int ONE_WARPS = 8, ONE_THREADS = ONE_WARPS * 32;
+__host__ __device__ constexpr int one_rows(int KP) { return KP <= 4 ? 16 : 8; }
+__host__ __device__ constexpr int one_pitch(int KP) { return ONE_WARPS * KP * 64 + 16; }  // rows of an ldmatrix in different banks
+__host__ __device__ constexpr int one_stages(int KP) { return KP >= 16 ? 3 : KP >= 8 ? 6 : KP >= 4 ? 3 : 4; }
+__host__ __device__ constexpr int one_out(int NT, int KP) { return NT == 1 && KP >= 16 ? 7 : 0; }
+__host__ __device__ constexpr int one_smem(int NT, int KP) {
+  return one_stages(KP) * one_rows(KP) * one_pitch(KP) + 2 * ONE_THREADS * NT * one_rows(KP) + ONE_THREADS * one_out(NT, KP) * 16;
+}
+// blocks per SM: the registers' 12 a column group and eight tokens, and the rings
+__host__ __device__ constexpr int one_blocks(int NT, int KP) { return NT * KP <= 2 ? 3 : NT * KP <= 4 ? 2 : 1; }
+
+template <int NT, int KP>
+__global__ void __launch_bounds__(ONE_THREADS, one_blocks(NT, KP))
+    ce_few_one_k(const bf16* __restrict__ h, const bf16* __restrict__ W, const int32_t* __restrict__ target, int T, int H,
+                 int V, int ldz, float* __restrict__ z, float2* __restrict__ stat, float* __restrict__ zt,
+                 float* __restrict__ slabs) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int NS = one_stages(KP), ROWS = one_rows(KP), RB = ROWS / 8, PITCH = one_pitch(KP), STAGE = ROWS * PITCH;
+  constexpr int OUT = one_out(NT, KP), IN = KP - OUT;
+  float2* parts = reinterpret_cast<float2*>(smem + NS * STAGE);  // [2][RB][NT][ONE_WARPS][32]
+  __shared__ uint64_t full[NS];
+  dep_launch();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int base = warp * KP * 32;
+  const int groups = (V + ROWS - 1) / ROWS;  // of rows: the blocks take them in turn
+  const int stages = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  auto row = [&](int k) { return (k * (int)gridDim.x + (int)blockIdx.x) * ROWS; };  // the first of stage k
+  bool failed = false;
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // what no copy writes and the products read: columns past the last, and the rows that a short last stage leaves of
+  // a part of the ring that no stage before it has filled
+  const int pad = PITCH / 16 - H / 8;
+  for (int i = tid; i < NS * ROWS * pad; i += ONE_THREADS)
+    *reinterpret_cast<uint4*>(smem + i / pad * PITCH + H * 2 + i % pad * 16) = make_uint4(0, 0, 0, 0);
+  const int last = min(ROWS, V - row(stages - 1));
+  if (stages <= NS)
+    for (int i = tid; i < (ROWS - last) * (H / 8); i += ONE_THREADS)
+      *reinterpret_cast<uint4*>(smem + (stages - 1) * STAGE + (last + i / (H / 8)) * PITCH + i % (H / 8) * 16) =
+          make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  auto fill = [&](int k) {  // the first warp
+    const int b = row(k), n = min(ROWS, V - b);
+    if (lane == 0) mbar_expect_tx(&full[k % NS], (uint32_t)n * (uint32_t)H * 2);
+    __syncwarp();
+    if (lane < n)
+      bulk_load(smem + (k % NS) * STAGE + lane * PITCH, W + (int64_t)(b + lane) * H, (uint32_t)H * 2, &full[k % NS]);
+    __syncwarp();
+  };
+  if (warp == 0)
+    for (int k = 0; k < min(stages, NS); ++k) fill(k);
+  uint4* held = reinterpret_cast<uint4*>(parts + 2 * RB * NT * ONE_THREADS) + tid;  // [OUT][ONE_THREADS], this thread's
+  uint32_t ha[IN][4 * NT];
+  float dh[KP][2][NT][4];
+#pragma unroll
+  for (int k = 0; k < KP; ++k) {
+    for (int i = 0; i < NT; ++i) {
+      uint32_t x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int col = base + 32 * k + 8 * j + 2 * c, t = g + 8 * i;
+        x[j] = t < T && col < H ? *reinterpret_cast<const uint32_t*>(h + (int64_t)t * H + col) : 0;
+        if (k < IN) ha[k < IN ? k : 0][4 * i + j] = x[j];
+        dh[k][j >> 1][i][2 * (j & 1)] = dh[k][j >> 1][i][2 * (j & 1) + 1] = 0.f;
+      }
+      if (k >= IN) held[(k - IN) * ONE_THREADS] = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+  }
+  int tgt[NT];
+  bool has[NT];
+  float m[NT], s[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    tgt[i] = g + 8 * i < T ? target[g + 8 * i] : -1;
+    has[i] = tgt[i] >= 0 && tgt[i] < V;
+    m[i] = -INFINITY;
+    s[i] = 0.f;
+  }
+  for (int k = 0; k < stages; ++k) {
+    const uint8_t* wp = smem + (k % NS) * STAGE + (lane & 7) * PITCH + (base + (lane >> 3) * 8) * 2;
+    reads_before_copies();  // those of the stage before, all used by now
+    mbar_wait(&full[k % NS], (uint32_t)(k / NS) & 1, failed);
+    float2* part = parts + (k & 1) * RB * NT * ONE_THREADS + lane;
+    float acc[RB][2][4];
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[b][0][q] = acc[b][1][q] = 0.f;
+#pragma unroll
+    for (int j = 0; j < KP; ++j) {
+      uint4 a, a8 = make_uint4(0, 0, 0, 0);
+      if (j < IN) {
+        const uint32_t* f = ha[j < IN ? j : 0];
+        a = make_uint4(f[0], f[1], f[2], f[3]);
+        if (NT > 1) a8 = make_uint4(f[4 * NT - 4], f[4 * NT - 3], f[4 * NT - 2], f[4 * NT - 1]);
+      } else {
+        a = held[(j - IN) * ONE_THREADS];
+      }
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        uint32_t w[4];
+        ldmatrix4(w, wp + b * 8 * PITCH + j * 64);
+        mma_bf16(acc[b][0], a.x, a8.x, a.y, a8.y, w[0], w[1]);
+        mma_bf16(acc[b][1], a.z, a8.z, a.w, a8.w, w[2], w[3]);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        part[((b * NT + i) * ONE_WARPS + warp) * 32] =
+            make_float2(acc[b][0][2 * i] + acc[b][1][2 * i], acc[b][0][2 * i + 1] + acc[b][1][2 * i + 1]);
+    __syncthreads();  // also: every warp is done with the stage before, which takes a new one
+    if (warp == 0 && k >= 1 && k - 1 + NS < stages) fill(k - 1 + NS);
+    uint32_t e[RB][NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int t = g + 8 * i, v0 = row(k) + 2 * c;  // this lane's rows: v0 + 8 b and the next
+      float2 x[RB];
+      float mn = m[i];
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        const int v = v0 + 8 * b;
+        x[b] = part[(b * NT + i) * ONE_WARPS * 32];
+#pragma unroll
+        for (int w = 1; w < ONE_WARPS; ++w) {
+          const float2 y = part[((b * NT + i) * ONE_WARPS + w) * 32];
+          x[b].x += y.x;
+          x[b].y += y.y;
+        }
+        if (warp == (k & (ONE_WARPS - 1)) && t < T && v < V) {
+          if (z) *reinterpret_cast<float2*>(z + (int64_t)t * ldz + v) = x[b];  // ldz > V, even
+          if (has[i] && (v == tgt[i] || v + 1 == tgt[i])) zt[t] = v == tgt[i] ? x[b].x : x[b].y;
+        }
+        if (has[i] && v < V) mn = fmaxf(mn, x[b].x);
+        if (has[i] && v + 1 < V) mn = fmaxf(mn, x[b].y);
+      }
+      mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 1));
+      mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
+      if (__any_sync(0xffffffffu, mn > m[i])) {  // the sums so far move to the new maximum
+        const float f = m[i] == -INFINITY ? 1.f : ex2((m[i] - mn) * kLog2e);
+        s[i] *= f;
+        m[i] = mn;
+        const float f0 = __shfl_sync(0xffffffffu, f, 8 * c), f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+#pragma unroll
+        for (int j = 0; j < KP; ++j)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            dh[j][q][i][0] *= f0;
+            dh[j][q][i][1] *= f1;
+            dh[j][q][i][2] *= f0;
+            dh[j][q][i][3] *= f1;
+          }
+      }
+      const float ref = mn == -INFINITY ? 0.f : mn;
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        const int v = v0 + 8 * b;
+        const float e0 = has[i] && v < V && v != tgt[i] ? ex2((x[b].x - ref) * kLog2e) : 0.f;
+        const float e1 = has[i] && v + 1 < V && v + 1 != tgt[i] ? ex2((x[b].y - ref) * kLog2e) : 0.f;
+        s[i] += e0 + e1;
+        // rounded for the mma: half a step of BF16 of each term of dh, as of d where tiles take it
+        const __nv_bfloat162 p = __floats2bfloat162_rn(e0, e1);
+        e[b][i] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+    }
+    if (!slabs) continue;
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int j = 0; j < KP; ++j) {
+        uint32_t w[4];
+        ldmatrix4_t(w, wp + b * 8 * PITCH + j * 64);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          mma_bf16_k8(dh[j][0][i], w[0], w[1], e[b][i]);
+          mma_bf16_k8(dh[j][1][i], w[2], w[3], e[b][i]);
+        }
+      }
+  }
+  if (failed && tid == 0) {  // what is on its way lands before the block's memory goes
+    const long long t0 = clock64();
+    while (clock64() - t0 < kWaitCycles) {
+    }
+  }
+  if (warp == 0) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      s[i] += __shfl_xor_sync(0xffffffffu, s[i], 1);
+      s[i] += __shfl_xor_sync(0xffffffffu, s[i], 2);
+      if (c == 0 && g + 8 * i < T) stat[(int64_t)(g + 8 * i) * gridDim.x + blockIdx.x] = make_float2(m[i], s[i]);
+    }
+  }
+  if (!slabs) return;
+  float* out = slabs + (int64_t)blockIdx.x * T * H;
+#pragma unroll
+  for (int k = 0; k < KP; ++k)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int col = base + 32 * k + 8 * q + g;
+      if (col >= H) continue;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int t = 8 * i + 2 * c + u;
+          if (t < T) out[(int64_t)t * H + col] = dh[k][q >> 1][i][2 * (q & 1) + u];
+        }
+    }
+}
+
+// A token's statistics from the blocks' (m, s), as in ce_join_k; one warp.
+struct FewStat {
+  float M, inv, at;  // maximum, 1 / S (0: no target), p - 1 at the target
+  int tgt;           // -1: none
+};
+__device__ __forceinline__ FewStat few_join(const float2* __restrict__ stat, int npieces, const float* __restrict__ zt,
+                                            const int32_t* __restrict__ target, int t, int T, int V, int lane,
+                                            float* row_loss) {
+  const int tgt = t < T ? target[t] : -1;
+  const bool has = tgt >= 0 && tgt < V;
+  float M = -INFINITY, rest = 0.f, S = 1.f;
+  if (has) {
+    const float2* st = stat + (int64_t)t * npieces;
+    for (int i = lane; i < npieces; i += 256) {  // eight loads at a time
+      float2 p[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) p[u] = i + 32 * u < npieces ? st[i + 32 * u] : make_float2(-INFINITY, 0.f);
+      float mn = M;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) mn = fmaxf(mn, p[u].x);
+      rest *= M == -INFINITY ? 1.f : expf(M - mn);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) rest += p[u].y * (p[u].x == -INFINITY ? 1.f : expf(p[u].x - mn));
+      M = mn;
+    }
+    const float wm = warp_max(M);
+    rest = warp_sum(rest * (M == -INFINITY ? 1.f : expf(M - wm)));
+    M = wm;
+    S = rest + expf(zt[t] - M);
+  }
+  if (row_loss && lane == 0 && t < T)
+    row_loss[t] = !has ? 0.f : zt[t] == M ? log1pf(rest) : (M - zt[t]) + logf(S);
+  return FewStat{M, has ? 1.f / S : 0.f, has ? -rest / S : 0.f, has ? tgt : -1};
+}
+
+// Token t's loss, and dh in 128 columns from col0 on from the blocks' sums; FEW_THREADS threads.
+__device__ __forceinline__ void ce_few_dh(const bf16* __restrict__ W, const int32_t* __restrict__ target, int t, int T,
+                                          int H, int V, int col0, const float2* __restrict__ stat, int npieces,
+                                          const float* __restrict__ zt, const float* __restrict__ slabs, float scale,
+                                          float* row_loss, bf16* __restrict__ dh) {
+  constexpr int NW = FEW_THREADS / 32;
+  __shared__ float4 part[NW][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = col0 + lane * 4;
+  const FewStat f = few_join(stat, npieces, zt, target, t, T, V, lane, warp == 0 && col0 == 0 ? row_loss : nullptr);
+  if (!dh) return;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (f.tgt >= 0 && col < H) {
+#pragma unroll 8
+    for (int r = warp; r < npieces; r += NW) {
+      const float m = stat[(int64_t)t * npieces + r].x, w = m == -INFINITY ? 1.f : expf(m - f.M);
+      const float4 u = *reinterpret_cast<const float4*>(slabs + ((int64_t)r * T + t) * H + col);
+      v.x += u.x * w;
+      v.y += u.y * w;
+      v.z += u.z * w;
+      v.w += u.w * w;
+    }
+  }
+  part[warp][lane] = v;
+  __syncthreads();
+  if (warp != 0 || col >= H) return;
+#pragma unroll
+  for (int w = 1; w < NW; ++w) {
+    const float4 u = part[w][lane];
+    v.x += u.x;
+    v.y += u.y;
+    v.z += u.z;
+    v.w += u.w;
+  }
+  uint2 o = make_uint2(0, 0);
+  if (f.tgt >= 0) {
+    const uint2 q = *reinterpret_cast<const uint2*>(W + (int64_t)f.tgt * H + col);
+    const __nv_bfloat162 w0 = *reinterpret_cast<const __nv_bfloat162*>(&q.x), w1 = *reinterpret_cast<const __nv_bfloat162*>(&q.y);
+    const __nv_bfloat162 a = __floats2bfloat162_rn(scale * (v.x * f.inv + f.at * __low2float(w0)),
+                                                   scale * (v.y * f.inv + f.at * __high2float(w0)));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(scale * (v.z * f.inv + f.at * __low2float(w1)),
+                                                   scale * (v.w * f.inv + f.at * __high2float(w1)));
+    o = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+  *reinterpret_cast<uint2*>(dh + (int64_t)t * H + col) = o;
+}
+
 // Block (x, y): rows [x per, (x + 1) per) of W, columns [512 y, 512 (y + 1)).
-__global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __restrict__ h, const bf16* __restrict__ W,
+// DH: dh as well, from W, into slabs.  Without it W is not read, and the first
+// first_y rows of blocks, if there are any, make the losses, and dh of what
+// ce_few_one_k left.
+template <bool DH>
+__global__ void __launch_bounds__(FEW_THREADS, DH ? 3 : 6) ce_few_bwd_k(const bf16* __restrict__ h, const bf16* __restrict__ W,
                                                               const int32_t* __restrict__ target, int T, int H, int V,
                                                               int ldz, const float* __restrict__ z,
                                                               const float2* __restrict__ stat, int npieces,
                                                               const float* __restrict__ zt, int per, float scale,
                                                               float* __restrict__ row_loss, float* __restrict__ slabs,
-                                                              bf16* __restrict__ dW) {
+                                                              bf16* __restrict__ dW, int first_y, bf16* __restrict__ dhout) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float sM[FEW_T], sI[FEW_T], sD[FEW_T];  // maximum, 1 / S (0: no target), p - 1 at the target
   __shared__ int sT[FEW_T];
   __shared__ uint64_t full[FEW_STAGES];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-  const int RG = few_groups(H), SUB = few_sub(H), WROW = few_wrow(H), STAGE = few_stage(T, H);
+  const int by = (int)blockIdx.y - first_y;
+  if (!DH && by < 0) {
+    const int q = blockIdx.y * gridDim.x + blockIdx.x, n = dhout ? (H + 127) / 128 : 1;
+    dep_launch();
+    dep_wait();
+    if (q < T * n) ce_few_dh(W, target, q / n, T, H, V, q % n * 128, stat, npieces, zt, slabs, scale, row_loss, dhout);
+    return;
+  }
+  const int RG = few_groups(H), SUB = few_sub(H), WROW = few_wrow(H), STAGE = few_stage(T, H, DH);
+  const int ZOFF = DH ? SUB * WROW : 0;  // the tokens' logits in a stage
   const int rg = warp / (4 / RG);  // this warp's row group
-  const int col0 = blockIdx.y * FEW_COLS, wcol = warp % (4 / RG) * 128, base = col0 + wcol;
+  const int col0 = by * FEW_COLS, wcol = warp % (4 / RG) * 128, base = col0 + wcol;
   const int ncol = min(128, H - base);  // this warp's columns: a multiple of 8, or none
   const int r0 = blockIdx.x * per, r1 = min(V, r0 + per), stages = (r1 - r0 + SUB - 1) / SUB;
   uint8_t* dbuf = smem + FEW_STAGES * STAGE;
@@ -504,9 +835,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __res
       hb[t][k] = lo | (hi << 16);
     }
   }
-  float dh[16][4];
+  float dh[DH ? 16 : 1][4];
+  if constexpr (DH) {
 #pragma unroll
-  for (int t = 0; t < 16; ++t) dh[t][0] = dh[t][1] = dh[t][2] = dh[t][3] = 0.f;
+    for (int t = 0; t < 16; ++t) dh[t][0] = dh[t][1] = dh[t][2] = dh[t][3] = 0.f;
+  }
   // the first warp: stage k's rows of W, and the tokens' logits of them (z's rows
   // are padded, so that whole stages may be read past V)
   auto fill = [&](int k) {
@@ -514,46 +847,25 @@ __global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __res
     uint64_t* bar = &full[k % FEW_STAGES];
     const int b = r0 + k * SUB, n = min(SUB, r1 - b);
     const uint32_t bytes = (uint32_t)min(FEW_COLS / RG, H - col0) * 2;
-    if (lane == 0) mbar_expect_tx(bar, (uint32_t)n * bytes + (uint32_t)(T * SUB) * 4);
+    if (lane == 0) mbar_expect_tx(bar, (DH ? (uint32_t)n * bytes : 0u) + (uint32_t)(T * SUB) * 4);
     __syncwarp();
-    for (int r = lane; r < n; r += 32) bulk_load(to + r * WROW, W + (int64_t)(b + r) * H + col0, bytes, bar);
-    if (lane < T) bulk_load(to + SUB * WROW + lane * SUB * 4, z + (int64_t)lane * ldz + b, (uint32_t)SUB * 4, bar);
+    if (DH)
+      for (int r = lane; r < n; r += 32) bulk_load(to + r * WROW, W + (int64_t)(b + r) * H + col0, bytes, bar);
+    if (lane < T) bulk_load(to + ZOFF + lane * SUB * 4, z + (int64_t)lane * ldz + b, (uint32_t)SUB * 4, bar);
     __syncwarp();
   };
   dep_wait();
   __syncthreads();
   if (warp == 0)
     for (int k = 0; k < min(stages, FEW_STAGES); ++k) fill(k);
-  for (int t = warp; t < FEW_T; t += FEW_THREADS / 32) {  // the tokens' statistics, as in ce_join_k
-    const int tgt = t < T ? target[t] : -1;
-    const bool has = tgt >= 0 && tgt < V;
-    float M = -INFINITY, rest = 0.f, S = 1.f;
-    if (has) {
-      const float2* st = stat + (int64_t)t * npieces;
-      for (int i = lane; i < npieces; i += 256) {  // eight loads at a time
-        float2 p[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) p[u] = i + 32 * u < npieces ? st[i + 32 * u] : make_float2(-INFINITY, 0.f);
-        float mn = M;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) mn = fmaxf(mn, p[u].x);
-        rest *= M == -INFINITY ? 1.f : expf(M - mn);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) rest += p[u].y * (p[u].x == -INFINITY ? 1.f : expf(p[u].x - mn));
-        M = mn;
-      }
-      const float wm = warp_max(M);
-      rest = warp_sum(rest * (M == -INFINITY ? 1.f : expf(M - wm)));
-      M = wm;
-      S = rest + expf(zt[t] - M);
-    }
+  for (int t = warp; t < FEW_T; t += FEW_THREADS / 32) {
+    const FewStat f = few_join(stat, npieces, zt, target, t, T, V, lane,
+                               blockIdx.x == 0 && blockIdx.y == 0 ? row_loss : nullptr);
     if (lane == 0) {
-      sM[t] = M;
-      sI[t] = has ? 1.f / S : 0.f;
-      sD[t] = has ? -rest / S : 0.f;
-      sT[t] = has ? tgt : -1;
-      if (t < T && blockIdx.x == 0 && blockIdx.y == 0)
-        row_loss[t] = !has ? 0.f : zt[t] == M ? log1pf(rest) : (M - zt[t]) + logf(S);
+      sM[t] = f.M;
+      sI[t] = f.inv;
+      sD[t] = f.at;
+      sT[t] = f.tgt;
     }
   }
   __syncthreads();
@@ -568,7 +880,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __res
       const int t = i / SUB, r = i % SUB;
       float d = 0.f;
       if (r < n && sT[t] >= 0) {
-        const float x = reinterpret_cast<const float*>(st + SUB * WROW)[t * SUB + r];
+        const float x = reinterpret_cast<const float*>(st + ZOFF)[t * SUB + r];
         d = b + r == sT[t] ? sD[t] : ex2((x - sM[t]) * kLog2e) * sI[t];
       }
       const bf16 v = __float2bfloat16_rn(d);
@@ -577,15 +889,16 @@ __global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __res
     }
     // rows past the last: their d is 0, but what an earlier stage left of W there
     // may be no number
-    for (int i = n * (WROW / 16) + tid; i < SUB * (WROW / 16); i += FEW_THREADS)
-      reinterpret_cast<uint4*>(smem + (k % FEW_STAGES) * STAGE)[i] = make_uint4(0, 0, 0, 0);
+    if (DH)
+      for (int i = n * (WROW / 16) + tid; i < SUB * (WROW / 16); i += FEW_THREADS)
+        reinterpret_cast<uint4*>(smem + (k % FEW_STAGES) * STAGE)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();  // also: every warp is done with the stage before, which takes a new one
     if (warp == 0 && k >= 1 && k - 1 + FEW_STAGES < stages) fill(k - 1 + FEW_STAGES);
     if (ncol <= 0 || rg * 16 >= n) continue;
-    uint32_t aT[4], aN[4];
+    uint32_t aT[4], aN[DH ? 4 : 1];
     // fragments of 16 by 16: lanes 0 .. 7 give the rows of the first 8 by 8 part, and so on
     ldmatrix4(aT, dT + (rg * 16 + (lane & 15)) * 16 + (lane >> 4) * 8);
-    ldmatrix4(aN, dN + (lane & 15) * SUB + rg * 16 + (lane >> 4) * 8);
+    if constexpr (DH) ldmatrix4(aN, dN + (lane & 15) * SUB + rg * 16 + (lane >> 4) * 8);
     const uint8_t* wp = st + (rg * 16 + (lane & 15)) * WROW + wcol * 2 + (lane >> 4) * 16;
 #pragma unroll
     for (int G = 0; G < 4; ++G) {
@@ -596,12 +909,14 @@ __global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __res
         o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
         mma_bf16(o[j], aT[0], aT[1], aT[2], aT[3], hb[4 * G + j][0], hb[4 * G + j][1]);
       }
+      if constexpr (DH) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t w[4];
-        ldmatrix4_t(w, wp + G * 64 + j * 32);
-        mma_bf16(dh[4 * G + 2 * j], aN[0], aN[1], aN[2], aN[3], w[0], w[1]);
-        mma_bf16(dh[4 * G + 2 * j + 1], aN[0], aN[1], aN[2], aN[3], w[2], w[3]);
+        for (int j = 0; j < 2; ++j) {
+          uint32_t w[4];
+          ldmatrix4_t(w, wp + G * 64 + j * 32);
+          mma_bf16(dh[4 * G + 2 * j], aN[0], aN[1], aN[2], aN[3], w[0], w[1]);
+          mma_bf16(dh[4 * G + 2 * j + 1], aN[0], aN[1], aN[2], aN[3], w[2], w[3]);
+        }
       }
       if (dW && 32 * G + 8 * c < ncol) {
 #pragma unroll
@@ -624,28 +939,29 @@ __global__ void __launch_bounds__(FEW_THREADS, 3) ce_few_bwd_k(const bf16* __res
     while (clock64() - t0 < kWaitCycles) {
     }
   }
-  if (!slabs) return;
-  if (RG > 1) {  // the row groups' parts, added in order through the ring's memory
-    float* part = reinterpret_cast<float*>(smem) + (int64_t)warp * 64 * 32 + lane;
-    __syncthreads();
-    if (rg > 0) {
+  if constexpr (DH) {
+    if (RG > 1) {  // the row groups' parts, added in order through the ring's memory
+      float* part = reinterpret_cast<float*>(smem) + (int64_t)warp * 64 * 32 + lane;
+      __syncthreads();
+      if (rg > 0) {
 #pragma unroll
-      for (int t = 0; t < 64; ++t) part[t * 32] = dh[t >> 2][t & 3];
+        for (int t = 0; t < 64; ++t) part[t * 32] = dh[t >> 2][t & 3];
+      }
+      __syncthreads();
+      if (rg > 0) return;
+      for (int q = 1; q < RG; ++q) {
+        const float* other = part + q * (4 / RG) * 64 * 32;
+#pragma unroll
+        for (int t = 0; t < 64; ++t) dh[t >> 2][t & 3] += other[t * 32];
+      }
     }
-    __syncthreads();
-    if (rg > 0) return;
-    for (int q = 1; q < RG; ++q) {
-      const float* other = part + q * (4 / RG) * 64 * 32;
+    float* out = slabs + (int64_t)blockIdx.x * T * H + base;
 #pragma unroll
-      for (int t = 0; t < 64; ++t) dh[t >> 2][t & 3] += other[t * 32];
+    for (int t = 0; t < 16; ++t) {
+      if (8 * t >= ncol) break;
+      if (g < T) *reinterpret_cast<float2*>(out + (int64_t)g * H + 8 * t + 2 * c) = make_float2(dh[t][0], dh[t][1]);
+      if (g + 8 < T) *reinterpret_cast<float2*>(out + (int64_t)(g + 8) * H + 8 * t + 2 * c) = make_float2(dh[t][2], dh[t][3]);
     }
-  }
-  float* out = slabs + (int64_t)blockIdx.x * T * H + base;
-#pragma unroll
-  for (int t = 0; t < 16; ++t) {
-    if (8 * t >= ncol) break;
-    if (g < T) *reinterpret_cast<float2*>(out + (int64_t)g * H + 8 * t + 2 * c) = make_float2(dh[t][0], dh[t][1]);
-    if (g + 8 < T) *reinterpret_cast<float2*>(out + (int64_t)(g + 8) * H + 8 * t + 2 * c) = make_float2(dh[t][2], dh[t][3]);
   }
 }
 
@@ -1498,8 +1814,17 @@ struct CeScratch {
   int npieces, runs, per;  // per: rows of W of a backward block, few tokens
   float* z;
   int ldz;
+  int kp;                // few tokens, W read once: column groups of a warp (0: W is read twice)
+  int dw_x, dw_per;      // blocks that make dW alone, and their rows of W
 };
 bool ce_few(int64_t T, int H) { return T <= FEW_T && (int64_t)few_held((int)T) * few_stride(H) <= FEW_SMEM; }
+// Column groups of a warp of ce_few_one_k: the least form that holds a row of H; 0: none does.
+int few_kp(int64_t T, int H) {
+  const int units = (H + 32 * ONE_WARPS - 1) / (32 * ONE_WARPS), most = T <= 8 ? 16 : 8;
+  int kp = 2;
+  while (kp < units) kp *= 2;
+  return kp <= most ? kp : 0;
+}
 size_t ce_carve(int64_t T, int H, int V, bool grads, bool dW, uint8_t* base, CeScratch* w) {
   size_t off = 0;
   auto take = [&](int64_t bytes) {
@@ -1514,18 +1839,28 @@ size_t ce_carve(int64_t T, int H, int V, bool grads, bool dW, uint8_t* base, CeS
     const int64_t smem = few_held((int)T) * few_stride(H), fit = FEW_SMEM / smem < 4 ? FEW_SMEM / smem : 4;
     const int sub = few_sub(H);
     const int64_t most = (V + FEW_ROWS - 1) / FEW_ROWS, ny = (H + FEW_COLS - 1) / FEW_COLS;
-    w->npieces = (int)(most < 152 * fit ? most : 152 * fit);
-    const int64_t bps = 226 * 1024 / (few_smem((int)T, H) + 1024) < 3 ? 2 : 3;
+    w->npieces = (int)(most < 152 * fit ? most : 152 * fit);  // where W is read twice
+    const int64_t bps = 226 * 1024 / (few_smem((int)T, H, true) + 1024) < 3 ? 2 : 3;
     int64_t nx = 152 * bps / ny > 0 ? 152 * bps / ny : 1;
     if (nx > (V + sub - 1) / sub) nx = (V + sub - 1) / sub;
     w->per = (int)up((V + nx - 1) / nx, sub);
     w->runs = (V + w->per - 1) / w->per;
     w->chunk = T;
     w->ldz = (int)up(V + sub, 64);
+    w->kp = few_kp(T, H);
+    if (w->kp) {
+      // as many blocks as run at once, of at least 16 rows each
+      const int64_t nb = 152 * one_blocks(few_held((int)T) / 8, w->kp), most = (V + 15) / 16;
+      w->npieces = (int)(most < nb ? most : nb);
+    }
+    int64_t dx = 152 * 6 / ny > 0 ? 152 * 6 / ny : 1;
+    if (dx > (V + sub - 1) / sub) dx = (V + sub - 1) / sub;
+    w->dw_per = (int)up((V + dx - 1) / dx, sub);
+    w->dw_x = (V + w->dw_per - 1) / w->dw_per;
     w->stat = (float2*)take(T * w->npieces * 8);
     w->zt = (float*)take(T * 4);
     w->z = grads ? (float*)take(T * w->ldz * 4) : nullptr;
-    w->slabs = grads ? (float*)take(w->runs * T * H * 4) : nullptr;
+    w->slabs = grads ? (float*)take((int64_t)(w->kp ? w->npieces : w->runs) * T * H * 4) : nullptr;
     return off;
   }
   w->chunk = ce_chunk(T, V);
@@ -1686,33 +2021,52 @@ cudaError_t launch_distill(const KdArgs& a, cudaStream_t s) {
   return a.target && a.tau != 1.f ? launch_distill2<CW, U, NS, BPS, true>(a, s) : launch_distill2<CW, U, NS, BPS, false>(a, s);
 }
 
-cudaError_t launch_few_bwd(const bf16* h, const bf16* W, const int32_t* target, int T, int H, int V, float g,
-                           float* row_loss, bf16* dh, bf16* dW, const CeScratch& w, cudaStream_t s) {
-  constexpr int DEV = 16, most = few_smem(FEW_T, 8) > few_smem(FEW_T, 512) ? few_smem(FEW_T, 8) : few_smem(FEW_T, 512);
-  static std::atomic<int> done[DEV];  // room for the largest ring, set once per device
+// Room for a kernel's shared memory, set once per device.
+template <auto KERNEL>
+cudaError_t allow_smem(int bytes) {
+  constexpr int DEV = 16;
+  static std::atomic<int> done[DEV];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && (dev >= DEV || !done[dev].load(std::memory_order_acquire))) {
-    e = cudaFuncSetAttribute(ce_few_bwd_k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess && dev < DEV) done[dev].store(1, std::memory_order_release);
   }
+  return e;
+}
+
+template <int NT, int KP>
+cudaError_t launch_few_one(const bf16* h, const bf16* W, const int32_t* target, int T, int H, int V, bool dh,
+                           const CeScratch& w, cudaStream_t s) {
+  const cudaError_t e = allow_smem<ce_few_one_k<NT, KP>>(one_smem(NT, KP));
   if (e != cudaSuccess) return e;
-  return launch(ce_few_bwd_k, dim3((unsigned)w.runs, (unsigned)((H + FEW_COLS - 1) / FEW_COLS)),
-                FEW_THREADS, (size_t)few_smem(T, H), 0, true, s, h, W, target, T, H, V, w.ldz, (const float*)w.z,
-                (const float2*)w.stat, w.npieces, (const float*)w.zt, w.per, g, row_loss, dh ? w.slabs : nullptr, dW);
+  return launch(ce_few_one_k<NT, KP>, dim3((unsigned)w.npieces), ONE_THREADS, (size_t)one_smem(NT, KP), 0, false, s, h, W,
+                target, T, H, V, w.ldz, w.z, w.stat, w.zt, dh ? w.slabs : nullptr);
+}
+
+// Losses and gradients from z and the blocks' statistics.
+cudaError_t launch_few_bwd(const bf16* h, const bf16* W, const int32_t* target, int T, int H, int V, float g,
+                           float* row_loss, bf16* dh, bf16* dW, const CeScratch& w, cudaStream_t s) {
+  const unsigned ny = (unsigned)((H + FEW_COLS - 1) / FEW_COLS);
+  if (dh && !w.kp) {
+    constexpr int a = few_smem(FEW_T, 8, true), b = few_smem(FEW_T, 512, true);  // the largest ring
+    const cudaError_t e = allow_smem<ce_few_bwd_k<true>>(a > b ? a : b);
+    if (e != cudaSuccess) return e;
+    return launch(ce_few_bwd_k<true>, dim3((unsigned)w.runs, ny), FEW_THREADS, (size_t)few_smem(T, H, true), 0, true, s, h,
+                  W, target, T, H, V, w.ldz, (const float*)w.z, (const float2*)w.stat, w.npieces, (const float*)w.zt, w.per,
+                  g, row_loss, w.slabs, dW, 0, (bf16*)nullptr);
+  }
+  const unsigned first = dh ? (unsigned)T * (unsigned)((H + 127) / 128) : dW ? 0u : (unsigned)T;
+  const unsigned nx = dW ? (unsigned)w.dw_x : first, fy = (first + nx - 1) / nx;
+  return launch(ce_few_bwd_k<false>, dim3(nx, fy + (dW ? ny : 0u)), FEW_THREADS, (size_t)few_smem(T, H, false), 0, true, s,
+                h, W, target, T, H, V, w.ldz, (const float*)w.z, (const float2*)w.stat, w.npieces, (const float*)w.zt,
+                w.dw_per, g, row_loss, w.slabs, dW, (int)fy, dh);
 }
 
 template <int HELD>
 cudaError_t launch_few_fwd(const bf16* h, const bf16* W, const int32_t* target, int T, int H, int V, const CeScratch& w,
                            cudaStream_t s) {
-  constexpr int DEV = 16;
-  static std::atomic<int> done[DEV];  // room for the widest h, set once per device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && (dev >= DEV || !done[dev].load(std::memory_order_acquire))) {
-    e = cudaFuncSetAttribute(ce_few_fwd_k<HELD>, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM);
-    if (e == cudaSuccess && dev < DEV) done[dev].store(1, std::memory_order_release);
-  }
+  const cudaError_t e = allow_smem<ce_few_fwd_k<HELD>>(FEW_SMEM);  // the widest h
   if (e != cudaSuccess) return e;
   return launch(ce_few_fwd_k<HELD>, dim3((unsigned)w.npieces), FEW_WARPS * 32, (size_t)HELD * few_stride(H), 0, false, s,
                 h, W, target, T, H, V, w.ldz, w.z, w.stat, w.zt);
@@ -1721,14 +2075,21 @@ cudaError_t launch_few_fwd(const bf16* h, const bf16* W, const int32_t* target, 
 // Linear cross-entropy of up to sixteen tokens.
 cudaError_t linear_ce_few(const bf16* h, const bf16* W, const int32_t* target, int T, int H, int V, float g,
                           float* row_loss, bf16* dh, bf16* dW, const CeScratch& w, cudaStream_t s) {
-  cudaError_t e = few_held(T) == 8 ? launch_few_fwd<8>(h, W, target, T, H, V, w, s)
-                                   : launch_few_fwd<16>(h, W, target, T, H, V, w, s);
-  if (e != cudaSuccess) return e;
-  if (!dh && !dW)
-    return launch(ce_join_k, dim3((unsigned)T), JOIN_THREADS, 0, 0, true, s, (const float2*)w.stat, w.npieces, target,
-                  (const float*)w.zt, V, row_loss, (uint16_t*)nullptr, (int64_t)0, (const bf16*)nullptr, (bf16*)nullptr, H);
-  e = launch_few_bwd(h, W, target, T, H, V, g, row_loss, dh, dW, w, s);
-  if (e != cudaSuccess || !dh) return e;
+  cudaError_t e = cudaErrorInvalidValue;
+  const bool d = dh != nullptr;
+  switch (T <= 8 ? w.kp : w.kp + 1) {
+    case 0: e = launch_few_fwd<8>(h, W, target, T, H, V, w, s); break;
+    case 1: e = launch_few_fwd<16>(h, W, target, T, H, V, w, s); break;
+    case 2: e = launch_few_one<1, 2>(h, W, target, T, H, V, d, w, s); break;
+    case 3: e = launch_few_one<2, 2>(h, W, target, T, H, V, d, w, s); break;
+    case 4: e = launch_few_one<1, 4>(h, W, target, T, H, V, d, w, s); break;
+    case 5: e = launch_few_one<2, 4>(h, W, target, T, H, V, d, w, s); break;
+    case 8: e = launch_few_one<1, 8>(h, W, target, T, H, V, d, w, s); break;
+    case 9: e = launch_few_one<2, 8>(h, W, target, T, H, V, d, w, s); break;
+    case 16: e = launch_few_one<1, 16>(h, W, target, T, H, V, d, w, s); break;
+  }
+  if (e == cudaSuccess) e = launch_few_bwd(h, W, target, T, H, V, g, row_loss, dh, dW, w, s);
+  if (e != cudaSuccess || !dh || w.kp) return e;
   const int64_t n4 = (int64_t)T * H / 4;
   return launch(ce_add_runs_k, dim3((unsigned)((n4 + 31) / 32)), RUN_WARPS * 32, 0, 0, true, s,
                 reinterpret_cast<const float4*>(w.slabs), n4, w.runs, g, reinterpret_cast<uint2*>(dh));
