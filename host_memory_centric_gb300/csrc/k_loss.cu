@@ -294,17 +294,19 @@ __global__ void __launch_bounds__(RUN_WARPS * 32) ce_add_runs_k(const float4* __
   dh[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// Up to sixteen tokens.  The products are then bound by reading W twice and
-// writing dW once, and their tiles' fixed costs weigh more than their work: of
-// a 256-row tile a few per cent would be tokens, and one token on a head of 448
-// by 93899 took 137 us of which the bytes need 25 (now 58).  So W is streamed
-// through registers:
-//   forward: z = h W^T by mma.sync (16 by 8 by 16; up to eight tokens leave half
+// Up to sixteen tokens.  The products are then bound by reading W and writing
+// dW, and their tiles' fixed costs weigh more than their work: of a 256-row tile
+// a few per cent would be tokens, and one token on a head of 448 by 93899 took
+// 137 us of which the bytes need 25 (now 41).  So W is streamed and multiplied
+// by mma.sync.  Two ways:
+//   one pass over W (ce_few_one_k) gives z, the statistics and the blocks' sums
+//   for dh, a second kernel the losses, dh, and dW = g d^T h from z;
+//   two passes, for rows that the first way does not hold or that are too narrow
+//   for it: z = h W^T (ce_few_fwd_k; 16 by 8 by 16, up to eight tokens leave half
 //   of its rows empty), one warp on 16 rows of W, h in shared memory; z goes to
 //   scratch in FP32 (16 rows at most) beside each block's (m, s) as in the
-//   softmax epilogue;
-//   backward: W comes through a ring of bulk copies, 16 rows by 512 columns a
-//   stage; dh += d W and dW = g d^T h by the same mma, d in BF16 as the tiles
+//   softmax epilogue; then dh += d W and dW = g d^T h by the same mma, W through
+//   a ring of bulk copies, 16 rows by 512 columns a stage, d in BF16 as the tiles
 //   take it (with fma in FP32 it was bound by issue slots: 412 us against 160
 //   for the forward with 11 tokens).
 constexpr int FEW_T = 16, FEW_WARPS = 8, FEW_ROWS = FEW_WARPS * 16;
@@ -468,36 +470,39 @@ __device__ __forceinline__ void mma_bf16_k8(float (&d)[4], uint32_t a0, uint32_t
 // needs p only up to a factor per token, so each block keeps sums of exp(z_v - m)
 // W_v around its running maximum m, moved when m rises, and ce_few_dh adds the
 // blocks' sums with their factors exp(m - M) / S.  W is then read once and dW
-// written once, which is the floor; with a second pass over W 5 tokens of 3584 by
-// 152064 took 558 us.  A stage is eight whole rows: the warps take a slice of the
-// columns each, h of it in registers as the first factor of z, the sums of dh in
+// written once, which is the floor: 5 tokens of 3584 by 152064 take 370 us of
+// 321 (with a second pass over W 558), dh alone 198 and the losses alone 159 of
+// 160.  A stage is 8 or 16 whole rows: the warps take a slice of the columns
+// each, h of it in registers as the first factor of z, the sums of dh in
 // registers too (their columns as the rows of the mma, tokens as its columns).
 // The warps' parts of z meet in shared memory, every warp adds them for itself in
 // the layout in which exp(z - m) is then its second factor of dh: one barrier a
-// stage.  W comes out of shared memory twice, once transposed.
-// NT: groups of eight tokens; KP: groups of 32 columns that a warp has.
+// stage.  W comes out of shared memory twice, once transposed.  16 rows where
+// rows are short (12 tokens of 1024 by 128256: 140 us, with 8 rows 157), four
+// warps up to 512 columns (8 of 512: 67, with eight warps of half the columns 71).
+// NT: groups of eight tokens; NW: warps; KP: groups of 32 columns that a warp has.
 // RB: groups of eight rows in a stage.  Of the last OUT column groups h stays in
-// shared memory, in the order of the fragments, where the registers do not reach.
-constexpr int ONE_WARPS = 8, ONE_THREADS = ONE_WARPS * 32;
+// shared memory, in the order of the fragments, where the registers do not reach
+// (spilled, 5 tokens of 3584 by 152064 took 440 us).
 __host__ __device__ constexpr int one_rows(int KP) { return KP <= 4 ? 16 : 8; }
-__host__ __device__ constexpr int one_pitch(int KP) { return ONE_WARPS * KP * 64 + 16; }  // rows of an ldmatrix in different banks
-__host__ __device__ constexpr int one_stages(int KP) { return KP >= 16 ? 3 : KP >= 8 ? 6 : KP >= 4 ? 3 : 4; }
+__host__ __device__ constexpr int one_pitch(int KP, int NW) { return NW * KP * 64 + 16; }  // an ldmatrix's rows in different banks
+__host__ __device__ constexpr int one_stages(int KP, int NW) { return NW == 4 ? 4 : KP == 8 ? 6 : 3; }
 __host__ __device__ constexpr int one_out(int NT, int KP) { return NT == 1 && KP >= 16 ? 7 : 0; }
-__host__ __device__ constexpr int one_smem(int NT, int KP) {
-  return one_stages(KP) * one_rows(KP) * one_pitch(KP) + 2 * ONE_THREADS * NT * one_rows(KP) + ONE_THREADS * one_out(NT, KP) * 16;
+__host__ __device__ constexpr int one_smem(int NT, int KP, int NW) {
+  return one_stages(KP, NW) * one_rows(KP) * one_pitch(KP, NW) + NW * 32 * (2 * NT * one_rows(KP) + one_out(NT, KP) * 16);
 }
 // blocks per SM: the registers' 12 a column group and eight tokens, and the rings
-__host__ __device__ constexpr int one_blocks(int NT, int KP) { return NT * KP <= 2 ? 3 : NT * KP <= 4 ? 2 : 1; }
+__host__ __device__ constexpr int one_blocks(int NT, int KP, int NW) { return NW == 4 ? 3 : NT * KP <= 4 ? 2 : 1; }
 
-template <int NT, int KP>
-__global__ void __launch_bounds__(ONE_THREADS, one_blocks(NT, KP))
+template <int NT, int KP, int NW>
+__global__ void __launch_bounds__(NW * 32, one_blocks(NT, KP, NW))
     ce_few_one_k(const bf16* __restrict__ h, const bf16* __restrict__ W, const int32_t* __restrict__ target, int T, int H,
                  int V, int ldz, float* __restrict__ z, float2* __restrict__ stat, float* __restrict__ zt,
                  float* __restrict__ slabs) {
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int NS = one_stages(KP), ROWS = one_rows(KP), RB = ROWS / 8, PITCH = one_pitch(KP), STAGE = ROWS * PITCH;
-  constexpr int OUT = one_out(NT, KP), IN = KP - OUT;
-  float2* parts = reinterpret_cast<float2*>(smem + NS * STAGE);  // [2][RB][NT][ONE_WARPS][32]
+  constexpr int NS = one_stages(KP, NW), ROWS = one_rows(KP), RB = ROWS / 8, PITCH = one_pitch(KP, NW), STAGE = ROWS * PITCH;
+  constexpr int OUT = one_out(NT, KP), IN = KP - OUT, NTH = NW * 32;
+  float2* parts = reinterpret_cast<float2*>(smem + NS * STAGE);  // [2][RB][NT][NW][32]
   __shared__ uint64_t full[NS];
   dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -513,11 +518,11 @@ __global__ void __launch_bounds__(ONE_THREADS, one_blocks(NT, KP))
   // what no copy writes and the products read: columns past the last, and the rows that a short last stage leaves of
   // a part of the ring that no stage before it has filled
   const int pad = PITCH / 16 - H / 8;
-  for (int i = tid; i < NS * ROWS * pad; i += ONE_THREADS)
+  for (int i = tid; i < NS * ROWS * pad; i += NTH)
     *reinterpret_cast<uint4*>(smem + i / pad * PITCH + H * 2 + i % pad * 16) = make_uint4(0, 0, 0, 0);
   const int last = min(ROWS, V - row(stages - 1));
   if (stages <= NS)
-    for (int i = tid; i < (ROWS - last) * (H / 8); i += ONE_THREADS)
+    for (int i = tid; i < (ROWS - last) * (H / 8); i += NTH)
       *reinterpret_cast<uint4*>(smem + (stages - 1) * STAGE + (last + i / (H / 8)) * PITCH + i % (H / 8) * 16) =
           make_uint4(0, 0, 0, 0);
   __syncthreads();
@@ -531,7 +536,7 @@ __global__ void __launch_bounds__(ONE_THREADS, one_blocks(NT, KP))
   };
   if (warp == 0)
     for (int k = 0; k < min(stages, NS); ++k) fill(k);
-  uint4* held = reinterpret_cast<uint4*>(parts + 2 * RB * NT * ONE_THREADS) + tid;  // [OUT][ONE_THREADS], this thread's
+  uint4* held = reinterpret_cast<uint4*>(parts + 2 * RB * NT * NTH) + tid;  // [OUT][NTH], this thread's
   uint32_t ha[IN][4 * NT];
   float dh[KP][2][NT][4];
 #pragma unroll
@@ -545,7 +550,7 @@ __global__ void __launch_bounds__(ONE_THREADS, one_blocks(NT, KP))
         if (k < IN) ha[k < IN ? k : 0][4 * i + j] = x[j];
         dh[k][j >> 1][i][2 * (j & 1)] = dh[k][j >> 1][i][2 * (j & 1) + 1] = 0.f;
       }
-      if (k >= IN) held[(k - IN) * ONE_THREADS] = make_uint4(x[0], x[1], x[2], x[3]);
+      if (k >= IN) held[(k - IN) * NTH] = make_uint4(x[0], x[1], x[2], x[3]);
     }
   }
   int tgt[NT];
@@ -562,7 +567,7 @@ __global__ void __launch_bounds__(ONE_THREADS, one_blocks(NT, KP))
     const uint8_t* wp = smem + (k % NS) * STAGE + (lane & 7) * PITCH + (base + (lane >> 3) * 8) * 2;
     reads_before_copies();  // those of the stage before, all used by now
     mbar_wait(&full[k % NS], (uint32_t)(k / NS) & 1, failed);
-    float2* part = parts + (k & 1) * RB * NT * ONE_THREADS + lane;
+    float2* part = parts + (k & 1) * RB * NT * NTH + lane;
     float acc[RB][2][4];
 #pragma unroll
     for (int b = 0; b < RB; ++b)
@@ -576,7 +581,7 @@ __global__ void __launch_bounds__(ONE_THREADS, one_blocks(NT, KP))
         a = make_uint4(f[0], f[1], f[2], f[3]);
         if (NT > 1) a8 = make_uint4(f[4 * NT - 4], f[4 * NT - 3], f[4 * NT - 2], f[4 * NT - 1]);
       } else {
-        a = held[(j - IN) * ONE_THREADS];
+        a = held[(j - IN) * NTH];
       }
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(ONE_THREADS, one_blocks(NT, KP))
     for (int b = 0; b < RB; ++b)
 #pragma unroll
       for (int i = 0; i < NT; ++i)
-        part[((b * NT + i) * ONE_WARPS + warp) * 32] =
+        part[((b * NT + i) * NW + warp) * 32] =
             make_float2(acc[b][0][2 * i] + acc[b][1][2 * i], acc[b][0][2 * i + 1] + acc[b][1][2 * i + 1]);
     __syncthreads();  // also: every warp is done with the stage before, which takes a new one
     if (warp == 0 && k >= 1 && k - 1 + NS < stages) fill(k - 1 + NS);
@@ -603,14 +608,14 @@ __global__ void __launch_bounds__(ONE_THREADS, one_blocks(NT, KP))
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
         const int v = v0 + 8 * b;
-        x[b] = part[(b * NT + i) * ONE_WARPS * 32];
+        x[b] = part[(b * NT + i) * NW * 32];
 #pragma unroll
-        for (int w = 1; w < ONE_WARPS; ++w) {
-          const float2 y = part[((b * NT + i) * ONE_WARPS + w) * 32];
+        for (int w = 1; w < NW; ++w) {
+          const float2 y = part[((b * NT + i) * NW + w) * 32];
           x[b].x += y.x;
           x[b].y += y.y;
         }
-        if (warp == (k & (ONE_WARPS - 1)) && t < T && v < V) {
+        if (warp == (k & (NW - 1)) && t < T && v < V) {
           if (z) *reinterpret_cast<float2*>(z + (int64_t)t * ldz + v) = x[b];  // ldz > V, even
           if (has[i] && (v == tgt[i] || v + 1 == tgt[i])) zt[t] = v == tgt[i] ? x[b].x : x[b].y;
         }
@@ -1814,16 +1819,21 @@ struct CeScratch {
   int npieces, runs, per;  // per: rows of W of a backward block, few tokens
   float* z;
   int ldz;
-  int kp;                // few tokens, W read once: column groups of a warp (0: W is read twice)
+  int one;               // few tokens: the form that reads W once (0: it is read twice)
   int dw_x, dw_per;      // blocks that make dW alone, and their rows of W
 };
 bool ce_few(int64_t T, int H) { return T <= FEW_T && (int64_t)few_held((int)T) * few_stride(H) <= FEW_SMEM; }
-// Column groups of a warp of ce_few_one_k: the least form that holds a row of H; 0: none does.
-int few_kp(int64_t T, int H) {
-  const int units = (H + 32 * ONE_WARPS - 1) / (32 * ONE_WARPS), most = T <= 8 ? 16 : 8;
-  int kp = 2;
-  while (kp < units) kp *= 2;
-  return kp <= most ? kp : 0;
+// The form of ce_few_one_k, its column groups of a warp times its warps: the
+// least that holds a row of H; 0: W is read twice, because no form does, or
+// because rows are so narrow that the barrier of a stage outweighs its work (7
+// tokens of 88 by 48042, losses alone: 7.0 us against 14.6 in one pass).
+int few_one(int64_t T, int H) {
+  const int groups = (H + 31) / 32;
+  return groups <= 4    ? 0
+         : groups <= 16 ? 4 * 4
+         : groups <= 32 ? 4 * 8
+         : groups <= 64 ? 8 * 8
+                        : groups <= 128 && T <= 8 ? 16 * 8 : 0;
 }
 size_t ce_carve(int64_t T, int H, int V, bool grads, bool dW, uint8_t* base, CeScratch* w) {
   size_t off = 0;
@@ -1847,20 +1857,22 @@ size_t ce_carve(int64_t T, int H, int V, bool grads, bool dW, uint8_t* base, CeS
     w->runs = (V + w->per - 1) / w->per;
     w->chunk = T;
     w->ldz = (int)up(V + sub, 64);
-    w->kp = few_kp(T, H);
-    if (w->kp) {
-      // as many blocks as run at once, of at least 16 rows each
-      const int64_t nb = 152 * one_blocks(few_held((int)T) / 8, w->kp), most = (V + 15) / 16;
+    w->one = few_one(T, H);
+    if (w->one) {
+      // as many blocks as run at once, of at least 32 rows each: each leaves a
+      // slab of dh to add (16 tokens of 256 by 8192: 16.7 us, with 16 rows 25.2)
+      const int nw = w->one == 16 ? 4 : 8;
+      const int64_t nb = 152 * one_blocks(few_held((int)T) / 8, w->one / nw, nw), most = (V + 31) / 32;
       w->npieces = (int)(most < nb ? most : nb);
     }
     int64_t dx = 152 * 6 / ny > 0 ? 152 * 6 / ny : 1;
-    if (dx > (V + sub - 1) / sub) dx = (V + sub - 1) / sub;
+    if (dx > (V + 2 * sub - 1) / (2 * sub)) dx = (V + 2 * sub - 1) / (2 * sub);
     w->dw_per = (int)up((V + dx - 1) / dx, sub);
     w->dw_x = (V + w->dw_per - 1) / w->dw_per;
     w->stat = (float2*)take(T * w->npieces * 8);
     w->zt = (float*)take(T * 4);
     w->z = grads ? (float*)take(T * w->ldz * 4) : nullptr;
-    w->slabs = grads ? (float*)take((int64_t)(w->kp ? w->npieces : w->runs) * T * H * 4) : nullptr;
+    w->slabs = grads ? (float*)take((int64_t)(w->one ? w->npieces : w->runs) * T * H * 4) : nullptr;
     return off;
   }
   w->chunk = ce_chunk(T, V);
@@ -2035,20 +2047,20 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
-template <int NT, int KP>
+template <int NT, int KP, int NW>
 cudaError_t launch_few_one(const bf16* h, const bf16* W, const int32_t* target, int T, int H, int V, bool dh,
                            const CeScratch& w, cudaStream_t s) {
-  const cudaError_t e = allow_smem<ce_few_one_k<NT, KP>>(one_smem(NT, KP));
+  const cudaError_t e = allow_smem<ce_few_one_k<NT, KP, NW>>(one_smem(NT, KP, NW));
   if (e != cudaSuccess) return e;
-  return launch(ce_few_one_k<NT, KP>, dim3((unsigned)w.npieces), ONE_THREADS, (size_t)one_smem(NT, KP), 0, false, s, h, W,
-                target, T, H, V, w.ldz, w.z, w.stat, w.zt, dh ? w.slabs : nullptr);
+  return launch(ce_few_one_k<NT, KP, NW>, dim3((unsigned)w.npieces), NW * 32, (size_t)one_smem(NT, KP, NW), 0, false, s, h,
+                W, target, T, H, V, w.ldz, w.z, w.stat, w.zt, dh ? w.slabs : nullptr);
 }
 
 // Losses and gradients from z and the blocks' statistics.
 cudaError_t launch_few_bwd(const bf16* h, const bf16* W, const int32_t* target, int T, int H, int V, float g,
                            float* row_loss, bf16* dh, bf16* dW, const CeScratch& w, cudaStream_t s) {
   const unsigned ny = (unsigned)((H + FEW_COLS - 1) / FEW_COLS);
-  if (dh && !w.kp) {
+  if (dh && !w.one) {
     constexpr int a = few_smem(FEW_T, 8, true), b = few_smem(FEW_T, 512, true);  // the largest ring
     const cudaError_t e = allow_smem<ce_few_bwd_k<true>>(a > b ? a : b);
     if (e != cudaSuccess) return e;
@@ -2077,19 +2089,19 @@ cudaError_t linear_ce_few(const bf16* h, const bf16* W, const int32_t* target, i
                           float* row_loss, bf16* dh, bf16* dW, const CeScratch& w, cudaStream_t s) {
   cudaError_t e = cudaErrorInvalidValue;
   const bool d = dh != nullptr;
-  switch (T <= 8 ? w.kp : w.kp + 1) {
+  switch (T <= 8 ? w.one : w.one + 1) {
     case 0: e = launch_few_fwd<8>(h, W, target, T, H, V, w, s); break;
     case 1: e = launch_few_fwd<16>(h, W, target, T, H, V, w, s); break;
-    case 2: e = launch_few_one<1, 2>(h, W, target, T, H, V, d, w, s); break;
-    case 3: e = launch_few_one<2, 2>(h, W, target, T, H, V, d, w, s); break;
-    case 4: e = launch_few_one<1, 4>(h, W, target, T, H, V, d, w, s); break;
-    case 5: e = launch_few_one<2, 4>(h, W, target, T, H, V, d, w, s); break;
-    case 8: e = launch_few_one<1, 8>(h, W, target, T, H, V, d, w, s); break;
-    case 9: e = launch_few_one<2, 8>(h, W, target, T, H, V, d, w, s); break;
-    case 16: e = launch_few_one<1, 16>(h, W, target, T, H, V, d, w, s); break;
+    case 16: e = launch_few_one<1, 4, 4>(h, W, target, T, H, V, d, w, s); break;
+    case 17: e = launch_few_one<2, 4, 4>(h, W, target, T, H, V, d, w, s); break;
+    case 32: e = launch_few_one<1, 4, 8>(h, W, target, T, H, V, d, w, s); break;
+    case 33: e = launch_few_one<2, 4, 8>(h, W, target, T, H, V, d, w, s); break;
+    case 64: e = launch_few_one<1, 8, 8>(h, W, target, T, H, V, d, w, s); break;
+    case 65: e = launch_few_one<2, 8, 8>(h, W, target, T, H, V, d, w, s); break;
+    case 128: e = launch_few_one<1, 16, 8>(h, W, target, T, H, V, d, w, s); break;
   }
   if (e == cudaSuccess) e = launch_few_bwd(h, W, target, T, H, V, g, row_loss, dh, dW, w, s);
-  if (e != cudaSuccess || !dh || w.kp) return e;
+  if (e != cudaSuccess || !dh || w.one) return e;
   const int64_t n4 = (int64_t)T * H / 4;
   return launch(ce_add_runs_k, dim3((unsigned)((n4 + 31) / 32)), RUN_WARPS * 32, 0, 0, true, s,
                 reinterpret_cast<const float4*>(w.slabs), n4, w.runs, g, reinterpret_cast<uint2*>(dh));
