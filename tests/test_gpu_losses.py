@@ -200,6 +200,49 @@ def test_linear_cross_entropy_gradient_matches_differences(T):
         assert abs(diff - float((d.double() * a).sum())) <= 4 * HALF * float((d.double().abs() * a.abs()).sum())
 
 
+# every form of the pass over W that up to sixteen tokens take, at its narrowest and its widest row and just beyond,
+# one stage of rows and less, stages that fill the ring exactly, more, and a last one that is not full
+@pytest.mark.parametrize("T,H,V", [(8, 136, 7), (1, 512, 32), (16, 504, 65), (9, 136, 30001), (5, 520, 16), (8, 1024, 14593),
+                                   (12, 1016, 777), (16, 1024, 9121), (8, 1032, 23), (3, 2048, 9121), (16, 2040, 3000),
+                                   (9, 1032, 1), (1, 2056, 25), (8, 4096, 2432), (5, 4088, 4870), (16, 2056, 700),
+                                   (8, 4104, 600)])
+def test_linear_cross_entropy_of_few_tokens(T, H, V):
+    h, W, tgt = lce_inputs(T, H, V, 16)
+    W *= torch.linspace(0.2, 2.0, V, device="cuda")[:, None]  # the maximum keeps rising along V
+    tgt[1::4] = -1
+    tgt[2::7] = V
+    full = run_lce(h, W, tgt, 1.0 / T)
+    check_lce(h, W, tgt, 1.0 / T, full)
+    for dh, dW in ((True, False), (False, True), (False, False)):
+        part = run_lce(h, W, tgt, 1.0 / T, dh, dW)
+        for a, b in zip(full, part):
+            assert b is None or torch.equal(a, b)
+    none = (tgt < 0) | (tgt >= V)
+    h[none] = float("nan")  # padding may hold anything
+    for a, b in zip(full, run_lce(h, W, tgt, 1.0 / T)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,H", [(4, 256), (12, 800), (8, 1200), (6, 3000)])
+def test_linear_cross_entropy_of_few_tokens_masked_and_confident(T, H):
+    """Rows of W that make logits of -inf and of some hundreds, and tokens whose target has all the probability."""
+    h, W, tgt = lce_inputs(T, H, 5000, 17)
+    h[:, 0] = 1.0
+    W[100:300] = 0
+    W[100:300, 0] = -float("inf")
+    W[7] = 0
+    W[7, 0] = 300.0
+    tgt[:] = 400
+    tgt[::2] = 7
+    loss, dh, dW = run_lce(h, W, tgt, 1.0)
+    z = h.double() @ W.double().t()
+    want = torch.logsumexp(z, 1) - z.gather(1, tgt.long()[:, None])[:, 0]
+    # logits of at most 300 of H products, as in check_lce; lse and loss are FP32 of that size, 2^-23 300 < 1e-4
+    assert float((loss.double() - want).abs().max()) <= 2 * (H / 8 + 2) * 2.0 ** -23 * 300 + 1e-4
+    assert bool((dW[100:300] == 0).all()) and bool(torch.isfinite(dW).all())
+    assert float(loss[::2].max()) == 0.0 and float(dW[7].float().abs().max()) > 0.5
+
+
 @pytest.mark.parametrize("T", [5, 600])
 def test_linear_cross_entropy_same_bits_twice_and_on_another_stream(T):
     h, W, tgt = lce_inputs(T, 256, 5000, 10)
