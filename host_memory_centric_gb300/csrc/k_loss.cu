@@ -1504,8 +1504,15 @@ struct BalArgs {
 constexpr int BAL_STAGES = 4;
 
 // Lanes that share a row, vectors a lane holds, rows a block has at a time.
-constexpr int bal_lanes(int E) { return E <= 8 ? 1 : E <= 16 ? 2 : E <= 32 ? 4 : E <= 64 ? 8 : E <= 128 ? 16 : 32; }
-constexpr int bal_rows(int E) { return BAL_THREADS / bal_lanes(E); }
+// With many long rows that come as vectors a lane holds two of them: the shuffles
+// and logarithms of a row weigh half as much (131072 rows of 128: 28.3 us against
+// 30.6, but 4096: 11.3 against 10.1).
+constexpr bool bal_wide(int64_t T, int E) { return E % 8 == 0 && (E > 256 || (E > 64 && T >= 32768)); }
+constexpr int bal_lanes(int64_t T, int E) {
+  const int e = bal_wide(T, E) ? E / 2 : E;
+  return e <= 8 ? 1 : e <= 16 ? 2 : e <= 32 ? 4 : e <= 64 ? 8 : e <= 128 ? 16 : 32;
+}
+constexpr int bal_rows(int64_t T, int E) { return BAL_THREADS / bal_lanes(T, E); }
 
 template <int LPR, int NV, bool VEC>
 __global__ void __launch_bounds__(BAL_THREADS, NV == 1 ? 2 : 1) balance_grad_k(const BalArgs a) {
@@ -1777,7 +1784,8 @@ inline int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 // many as fit kPieceBytes, at least 1024 (a chunk re-reads the weights for
 // every product, so short chunks are bound by memory), the chunks of one call
 // equal up to the 256-row tile.
-constexpr int64_t kBalBlocks = 304;  // two blocks of 512 threads on each SM
+// the blocks of 512 threads that the SMs hold at once
+constexpr int64_t bal_blocks(int64_t T, int E) { return bal_wide(T, E) && E <= 256 ? 152 : 304; }
 constexpr int64_t kPieceBytes = (int64_t)3 << 30;
 int64_t ce_chunk(int64_t T, int V) {
   int64_t most = kPieceBytes / (2 * up(V, 64)) / 256 * 256;
@@ -1910,8 +1918,8 @@ size_t bal_carve(int64_t T, int S, int E, uint8_t* base, BalScratch* w) {
     return p;
   };
   const int64_t G = T / S;
-  int64_t blk = (kBalBlocks + G - 1) / G;
-  const int64_t most = (S + bal_rows(E) - 1) / bal_rows(E);  // a block has all its lanes' rows to take
+  int64_t blk = (bal_blocks(T, E) + G - 1) / G;
+  const int64_t most = (S + bal_rows(T, E) - 1) / bal_rows(T, E);  // a block has all its lanes' rows to take
   if (blk > most) blk = most;
   w->rows = (int)((S + blk - 1) / blk);
   w->nblk = (S + w->rows - 1) / w->rows;
@@ -1957,16 +1965,16 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, in
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int LPR, int NV>
+template <int LPR, int NV, bool VEC>
 cudaError_t launch_balance_grad(const BalArgs& a, cudaStream_t s) {
   const dim3 grid((unsigned)a.nblk, (unsigned)a.G);
-  if (a.E % 8) return launch(balance_grad_k<LPR, NV, false>, grid, BAL_THREADS, 0, 0, true, s, a);
+  if (!VEC) return launch(balance_grad_k<LPR, NV, VEC>, grid, BAL_THREADS, 0, 0, true, s, a);
   constexpr int DEV = 16;
   static std::atomic<int> done[DEV];  // room for the whole ring, set once per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && (dev >= DEV || !done[dev].load(std::memory_order_acquire))) {
-    e = cudaFuncSetAttribute(balance_grad_k<LPR, NV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(balance_grad_k<LPR, NV, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(BAL_STAGES * (size_t)BAL_THREADS * NV * 32));
     if (e == cudaSuccess && dev < DEV) done[dev].store(1, std::memory_order_release);
   }
@@ -1974,7 +1982,7 @@ cudaError_t launch_balance_grad(const BalArgs& a, cudaStream_t s) {
   // no more stages than the block has chunks for
   const int chunks = (a.rows + BAL_THREADS / LPR - 1) / (BAL_THREADS / LPR);
   const size_t smem = (size_t)(BAL_THREADS / LPR) * a.E * 4 * (chunks < BAL_STAGES ? chunks : BAL_STAGES);
-  return launch(balance_grad_k<LPR, NV, true>, grid, BAL_THREADS, smem, 0, true, s, a);
+  return launch(balance_grad_k<LPR, NV, VEC>, grid, BAL_THREADS, smem, 0, true, s, a);
 }
 
 // The join and the sum of runs stand between two GEMMs that use nearly all
@@ -2231,13 +2239,26 @@ cudaError_t router_balance(const float* logits, const int32_t* idx, const uint8_
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const BalArgs a{logits, valid, G, S, E, k, w.rows, w.nblk, w.ldp, alpha / (float)G, z_coef / (float)G, w.nparts,
                   w.parts, counts, dlogits, prob, loss, w.partial, w.gloss, w.ticket};
-  if (E <= 8) return launch_balance_grad<1, 1>(a, s);
-  if (E <= 16) return launch_balance_grad<2, 1>(a, s);
-  if (E <= 32) return launch_balance_grad<4, 1>(a, s);
-  if (E <= 64) return launch_balance_grad<8, 1>(a, s);
-  if (E <= 128) return launch_balance_grad<16, 1>(a, s);
-  if (E <= 256) return launch_balance_grad<32, 1>(a, s);
-  return launch_balance_grad<32, 2>(a, s);
+  const int lanes = bal_lanes(T, E);
+  if (bal_wide(T, E)) {
+    if (lanes == 8) return launch_balance_grad<8, 2, true>(a, s);
+    if (lanes == 16) return launch_balance_grad<16, 2, true>(a, s);
+    return launch_balance_grad<32, 2, true>(a, s);
+  }
+  if (E % 8 == 0) {
+    if (lanes == 1) return launch_balance_grad<1, 1, true>(a, s);
+    if (lanes == 2) return launch_balance_grad<2, 1, true>(a, s);
+    if (lanes == 4) return launch_balance_grad<4, 1, true>(a, s);
+    if (lanes == 8) return launch_balance_grad<8, 1, true>(a, s);
+    if (lanes == 16) return launch_balance_grad<16, 1, true>(a, s);
+    return launch_balance_grad<32, 1, true>(a, s);
+  }
+  if (lanes == 1) return launch_balance_grad<1, 1, false>(a, s);
+  if (lanes == 2) return launch_balance_grad<2, 1, false>(a, s);
+  if (lanes == 4) return launch_balance_grad<4, 1, false>(a, s);
+  if (lanes == 8) return launch_balance_grad<8, 1, false>(a, s);
+  if (lanes == 16) return launch_balance_grad<16, 1, false>(a, s);
+  return E <= 256 ? launch_balance_grad<32, 1, false>(a, s) : launch_balance_grad<32, 2, false>(a, s);
 }
 
 cudaError_t loss_error_read(int* code, int clear) {

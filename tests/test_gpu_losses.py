@@ -586,6 +586,15 @@ def test_router_balance_same_bits_twice_and_captured(T, S, E, k):
         assert torch.equal(x, y) and torch.equal(x, o)
 
 
+# many rows, where a lane holds two vectors of a row, and just too few of them; a last block and chunk that are not full
+@pytest.mark.parametrize("T,S,E,k", [(32768, 32768, 72, 4), (32767, 32767, 72, 4), (40000, 2500, 128, 8), (36000, 3600, 136, 2),
+                                     (33000, 33000, 256, 8), (32768, 4096, 68, 3)])
+def test_router_balance_many_rows(T, S, E, k):
+    z, idx = bal_inputs(T, E, k, 136)
+    valid = (torch.rand(T, generator=gen(137), device="cuda") > 0.1).to(torch.uint8)
+    check_bal(z, idx, valid, S, 0.01, 0.001, run_bal(z, idx, valid, S, 0.01, 0.001))
+
+
 def test_router_balance_refilled_ring_under_load():
     z, idx = bal_inputs(131072, 128, 8, 135)
     want = run_bal(z, idx, None, 32768, 0.01, 0.001)
