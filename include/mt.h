@@ -455,7 +455,9 @@ mt_status mt_cross_entropy(void* logits, const int32_t* target, int64_t rows, in
  * in pieces of 128 columns as the product's tiles come out; for the gradients
  * the exponentials of a bounded chunk of tokens (up to 3 GiB) are held in 16
  * bits, relative to each piece's maximum, so their error does not grow with
- * the logits; over several chunks dW is summed in FP32.  scratch: 256-byte
+ * the logits; over several chunks dW is summed in FP32.  Up to 16 tokens W is
+ * streamed instead, once where H <= 4096 (2048 from 9 tokens on), and only the
+ * logits are held, in FP32.  scratch: 256-byte
  * aligned device memory of
  * mt_linear_cross_entropy_scratch_bytes(T, H, V, dh or dW wanted) bytes, not
  * shared by calls that may overlap.  H a multiple of 8, V <= 2097152, h, W, dh
