@@ -2191,14 +2191,19 @@ cudaError_t distill_topk(const bf16* logits, const int32_t* target, const float*
   //   many rows: one warp and 12 blocks per SM up to 7168 columns (16384 rows of
   //   7000: 114 against 118 with two warps; 8192 rows of 10000: 81 against 67),
   //   two up to 15360 (8192 rows of 14336: 95 against 98 with four; of 16384: 110
-  //   against 101), four up to 24576, with two temperatures, where the
-  //   exponentials weigh more, up to 40960 (8192 rows of 28000: 177 against 170
-  //   with eight; 4096 of 36000 with two temperatures: 113 against 129, of 45000:
-  //   161 against 149), eight up to 65536 (4096 rows of 64000: 194 against 208
-  //   with sixteen; of 80000: 252 against 214, where two rows per SM no longer
-  //   stay in L2 until they are read again)
+  //   against 101), four up to 26624 (3000 rows of 26000: 58 against 69 with
+  //   eight; 8192 of 28000: 177 against 170), with two temperatures, where the
+  //   exponentials weigh more, up to 40960 (3000 of 36000: 84 against 97; 4096 of
+  //   45000: 161 against 149), eight up to 61440 (4096 rows of 58000: 174 against
+  //   176 with sixteen, of 65000: 204 against 184), with two temperatures up to
+  //   73728 (of 70000: 214 against 239; of 80000: 252 against 214, where two rows
+  //   per SM no longer stay in L2 until they are read again)
   const bool two = target && tau != 1.f;
-  int warps = V <= 7168 ? 1 : V <= 15360 ? 2 : V <= (two ? 40960 : 24576) ? 4 : V <= 65536 ? 8 : 16;
+  int warps = V <= 7168 ? 1 : V <= 15360 ? 2 : V <= (two ? 40960 : 26624) ? 4 : V <= (two ? 73728 : 61440) ? 8 : 16;
+  //   rows for two turns of four warps' 608 blocks: four further on (1216 rows of
+  //   36000: 35 against 39 with eight; 1500 of 42000: 51 against 48), for one turn
+  //   too (500 rows of 58000: 24 against 27; 600 of 64000: 34 against 31)
+  if (warps == 8 && V <= (rows <= 608 ? 61440 : rows <= 1216 ? 45056 : 0)) warps = 4;
   //   few rows, so that a row's own time counts: four warps while their 608
   //   blocks take all rows at once (304 rows of 4096: 4.6 against 6.7 with one;
   //   600: 7.8 against 9.2; 1200: 11.4 against 10.4), eight while 304 do (152 rows
