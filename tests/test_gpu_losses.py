@@ -461,6 +461,16 @@ def test_distill_refilled_rings_under_load(R, V, tau, hard):
             assert (a is None and b is None) or torch.equal(a, b)
 
 
+# the gradient over the logits, row ends off the vectors, rows held by the ring and rows fetched a second time
+@pytest.mark.parametrize("R,V,tau,hard", [(4096, 20001, 1.0, True), (4096, 32003, 2.0, True), (1024, 152067, 1.5, False)])
+def test_distill_in_place_under_load(R, V, tau, hard):
+    z, tgt, y, ids = kd_inputs(R, V, 40, 96, hard)
+    want = run_kd(z, tgt, y, ids, tau, 0.4, 0.6)
+    for _ in range(5):
+        for a, b in zip(run_kd(z, tgt, y, ids, tau, 0.4, 0.6, in_place=True), want):
+            assert (a is None and b is None) or torch.equal(a, b)
+
+
 def test_distill_gradient_matches_differences():
     z, tgt, y, ids = kd_inputs(6, 300, 7, 90)
     _, _, d = run_kd(z, tgt, y, ids, 1.5, 0.5, 1.0)
